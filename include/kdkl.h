@@ -290,6 +290,167 @@ kd_status kd_lmhead_topk(const kd_topk_problem* prob, const uint16_t* H, const u
                          int32_t* topk_idx, float* topk_logit, void* workspace,
                          size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Tuning the head by preferences or by a policy. Four calls, in the order in
+ * which a training step makes them: the log-probabilities of given tokens, a
+ * loss over them with its gradient, the way back to dH and dW, and the
+ * optimizer's step. As above: device pointers, no allocation, asynchronous on
+ * `stream`, device-detected errors through kd_kl_check_status(workspace).
+ *
+ * Token log-probabilities of the LM head, the logits never stored:
+ *   z = H W^T / tau,  lse[t] = log sum_v exp(z[t,v]),  logp[t] = z[t,ids[t]] - lse[t]
+ *   dL/dz[t,v] = g[t] (onehot(ids[t])[v] - softmax(z[t])[v]),  g = dL/dlogp
+ *   dH = dL/dz . W / tau,  dW = (dL/dz)^T . H / tau */
+typedef struct {
+  int64_t T;          /* tokens (rows of H) */
+  int64_t d;          /* hidden size; multiple of 8 */
+  int64_t V;          /* vocabulary (rows of W) */
+  float temperature;  /* tau > 0 */
+  int32_t dw_bf16;    /* backward: dW is bf16 [V, d] instead of fp32 (not accumulated) */
+  int64_t chunk;      /* backward: the gradient-of-logits buffer is bounded as in kd_kl_problem */
+} kd_logprob_problem;
+
+/* Workspace bytes of the forward (which = 0) or the backward (which = 1);
+ * linear in T; 0 if the problem is invalid. */
+size_t kd_logprob_workspace_size(const kd_logprob_problem* prob, int which);
+
+/*   ids   [T] int32            the token whose log-probability is wanted, in [0, V)
+ *   mask  [T] uint8 or NULL    nonzero = wanted; the others' logp and lse read 0,
+ *                              their ids are not read and no product is computed
+ *   logp  [T] fp32 out,  lse [T] fp32 out
+ * A wanted id outside [0, V) is reported as KD_ERR_INDEX_RANGE by
+ * kd_kl_check_status. */
+kd_status kd_logprob_forward(const kd_logprob_problem* prob, const uint16_t* H, const uint16_t* W,
+                             const int32_t* ids, const uint8_t* mask, float* logp, float* lse,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/*   lse        [T] fp32        from kd_logprob_forward on the same inputs
+ *   grad_logp  [T] fp32        dL/dlogp. A token whose gradient is zero (masked,
+ *                              clipped) contributes nothing: it is left out of every
+ *                              product, its id and lse are not read, its dH row is zero
+ *   dH         [T, d] bf16 out
+ *   dW         [V, d] out      fp32, overwritten or (accumulate_dW) added to; or bf16
+ *                              when prob->dw_bf16 (accumulate_dW must be 0)
+ * The gradient of the logits is rounded to bf16 before it enters the two
+ * products, as in kd_kl_backward: dH and dW carry that relative 2^-8 per term. */
+kd_status kd_logprob_backward(const kd_logprob_problem* prob, const uint16_t* H, const uint16_t* W,
+                              const int32_t* ids, const float* lse, const float* grad_logp,
+                              uint16_t* dH, void* dW, int accumulate_dW, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/* Clipped policy loss with a KL term. Per counted token, with r =
+ * exp(logp - old_logp), A its advantage, x = ref_logp - logp:
+ *   surrogate  s = min(r A, clip(r, 1 - clip_low, 1 + clip_high) A)
+ *              and, when A < 0 and dual_clip > 0, s = max(s, dual_clip A)
+ *   penalty    k = e^x - 1 - x
+ *   loss = sum_t w[t] (-s[t] + kl_coef k[t])
+ * with w = 1 / N (KD_REDUCE_TOKEN; N counted tokens), 1 / (S' n_s)
+ * (KD_REDUCE_SEQUENCE: the mean over the S' sequences that have counted
+ * tokens, of each one's mean over its n_s), or 1 / norm (KD_REDUCE_SUM).
+ *   dloss/dlogp = w (-A r [r not clipped] + kl_coef (1 - e^x))
+ * On which side of a border a ratio is, is decided in 48 bits of logp - old_logp. */
+enum { KD_REDUCE_TOKEN = 0, KD_REDUCE_SEQUENCE = 1, KD_REDUCE_SUM = 2 };
+
+typedef struct {
+  int64_t T;         /* tokens, below 2^31 - 4096 */
+  int64_t S;         /* sequences; 0 without cu_seqlens */
+  double clip_low;   /* in [0, 1] */
+  double clip_high;  /* >= 0 */
+  double dual_clip;  /* > 1, or 0: off */
+  double kl_coef;    /* finite; 0 without ref_logp */
+  double norm;       /* KD_REDUCE_SUM: > 0 */
+  int32_t reduction;
+  int32_t advantage_per_sequence; /* advantages are [S], else [T] */
+} kd_policy_problem;
+
+size_t kd_policy_workspace_size(const kd_policy_problem* prob);
+
+/*   logp, old_logp, ref_logp  [T] fp32; old_logp NULL: ratio 1 (on-policy);
+ *                             ref_logp NULL: no penalty
+ *   advantages  [T] or [S] fp32
+ *   mask        [T] uint8 or NULL   what lies in uncounted places is never used
+ *   cu_seqlens  [S+1] int32 or NULL  sequence s is tokens [cu[s], cu[s+1]): from 0 to T,
+ *               never falling (empty sequences allowed); needed, and read, for
+ *               KD_REDUCE_SEQUENCE and advantages per sequence only.
+ *               Otherwise KD_ERR_INVALID_ARG through kd_kl_check_status
+ *   grad_loss   upstream gradient (host scalar)
+ *   loss        [1] fp32 out (0 when nothing counts)
+ *   stats       [3] fp32 out or NULL   sum w (-s), sum w k, share of counted tokens clipped
+ *   grad_logp   [T] fp32 out or NULL   grad_loss * dloss/dlogp (0 where not counted)
+ * Sums have a fixed order: results are the same from run to run. */
+kd_status kd_policy_loss(const kd_policy_problem* prob, const float* logp, const float* old_logp,
+                         const float* ref_logp, const float* advantages, const uint8_t* mask,
+                         const int32_t* cu_seqlens, float grad_loss, float* loss, float* stats,
+                         float* grad_logp, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Preference loss over pairs (chosen, rejected) of sequences:
+ *   q_s = sum over s's counted tokens of (logp - ref_logp), divided by their
+ *         number when average != 0 (an empty sequence has q = 0)
+ *   h = q_chosen - q_rejected - margin
+ *   KD_PREF_SIGMOID  -(1 - e) log sigma(beta h) - e log sigma(-beta h), e = label_smoothing
+ *   KD_PREF_IPO      (h - 1 / (2 beta))^2
+ *   KD_PREF_HINGE    max(0, 1 - beta h)
+ *   loss = mean over the P pairs */
+enum { KD_PREF_SIGMOID = 0, KD_PREF_IPO = 1, KD_PREF_HINGE = 2 };
+
+typedef struct {
+  int64_t T;               /* tokens, below 2^31 - 4096 */
+  int64_t P;               /* pairs: 2 P sequences, 2 P < 2^31 - 1 */
+  double beta;             /* > 0 */
+  double label_smoothing;  /* in [0, 1) */
+  double margin;
+  int32_t kind;
+  int32_t average;
+  int32_t halves;          /* 0: sequences 2i (chosen) and 2i+1; else i and P + i */
+  int32_t reserved;        /* set to 0 */
+} kd_pref_problem;
+
+size_t kd_pref_workspace_size(const kd_pref_problem* prob);
+
+/*   logp, ref_logp [T] fp32 (ref_logp NULL: 0), mask [T] uint8 or NULL,
+ *   cu_seqlens [2P+1] int32 as in kd_policy_loss
+ *   loss      [1] fp32 out
+ *   rewards   [P, 2] fp32 out       beta q of the chosen and of the rejected sequence
+ *   grad_logp [T] fp32 out or NULL  grad_loss * dloss/dlogp */
+kd_status kd_pref_loss(const kd_pref_problem* prob, const float* logp, const float* ref_logp,
+                       const uint8_t* mask, const int32_t* cu_seqlens, float grad_loss, float* loss,
+                       float* rewards, float* grad_logp, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
+/* One AdamW step over a list of tensors, in one launch for up to 384 of them:
+ *   m = beta1 m + (1 - beta1) g s,  v = beta2 v + (1 - beta2) (g s)^2
+ *   p = p (1 - lr weight_decay [decay]) - lr / (1 - beta1^step)
+ *         * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * with s = grad_scale (times *grad_scale_dev). All tensors of a call have the
+ * same types. With state_8bit, exp_avg holds m and exp_avg_sq holds sqrt(v) as
+ * e4m3 bytes, and every 256 consecutive elements of a tensor share one fp32
+ * power of two in m_scale / v_scale (ceil(n / 256) of them): value = code *
+ * scale. Zero bytes and scales of 1 are the state of a first step. */
+typedef struct {
+  void* param;       /* [n] fp32 or bf16, updated */
+  const void* grad;  /* [n] fp32 or bf16 */
+  void* exp_avg;     /* [n] fp32, or e4m3 bytes */
+  void* exp_avg_sq;  /* [n] fp32 (v), or e4m3 bytes (sqrt(v)) */
+  uint16_t* copy;    /* [n] bf16 out: the new parameters rounded; or NULL */
+  float* m_scale;    /* state_8bit: [ceil(n/256)] */
+  float* v_scale;
+  int64_t n;         /* elements, >= 0 */
+  int32_t decay;     /* nonzero: weight_decay applies */
+  int32_t reserved;  /* set to 0 */
+} kd_adamw_tensor;
+
+typedef struct {
+  double lr, beta1, beta2, eps, weight_decay;
+  int64_t step;                  /* this step's number, from 1 */
+  const float* grad_scale_dev;   /* device scalar or NULL (a clip coefficient) */
+  float grad_scale;
+  int32_t param_bf16, grad_bf16, state_8bit;
+} kd_adamw_options;
+
+/* `tensors` is a host array; it is read before the call returns. */
+kd_status kd_adamw_step(const kd_adamw_tensor* tensors, int32_t n_tensors,
+                        const kd_adamw_options* opts, void* stream);
+
 /* BLOCKING: synchronises `stream`, then returns the first device-detected
  * error recorded in `workspace` by the latest call that used it (KD_OK if
  * none). Each forward/backward call clears the record when it starts. */

@@ -17,7 +17,7 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_NAME = "libkdkl.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 SOURCES = ["kernels_gemm.cu", "kernels_small.cu", "kernels_rkl.cu", "kdkl_api.cu",
-           "kdkl_noalloc.cu"]
+           "kdkl_noalloc.cu", "kernels_policy.cu", "kernels_adamw.cu", "kdkl_tune.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -116,6 +116,17 @@ kd_status device_info(DeviceInfo* out) {
   return di.supported ? KD_OK : KD_ERR_UNSUPPORTED;
 }
 
+}  // namespace
+
+int current_device(int* num_sms) {
+  DeviceInfo di;
+  const kd_status st = device_info(&di);
+  *num_sms = di.num_sms;
+  return st;
+}
+
+namespace {
+
 kd_status get_encoder() {
   std::call_once(g_encode_once, [] {
     void* fn = nullptr;
@@ -252,12 +263,15 @@ bool problem_ok(const kd_kl_problem* p) {
   return true;
 }
 
-FwdPlan plan_forward(const kd_kl_problem& p, int num_sms, bool pair, int procs, bool mix = false) {
+// split_tiles: vocabulary tiles per unit, 0 = the default.
+FwdPlan plan_forward(const kd_kl_problem& p, int num_sms, bool pair, int procs, bool mix = false,
+                     int split_tiles = 0) {
   (void)num_sms;
   FwdPlan f{};
   const int tile_m = pair ? 2 * BM : BM;
   f.pair = pair;
-  const LogitPlan lp = plan_logit(p.T, p.V, p.d, tile_m, fwd_split_tiles());
+  const LogitPlan lp = plan_logit(p.T, p.V, p.d, tile_m,
+                                  split_tiles > 0 ? split_tiles : fwd_split_tiles());
   f.m_tiles = lp.m_tiles;
   f.n_tiles = lp.n_tiles;
   f.nsplit = p.T > 0 ? lp.nsplit : 1;
@@ -291,9 +305,9 @@ struct BlockPlan {
   int64_t Tb, Vb, n_tblocks, n_vblocks;
 };
 
-BlockPlan slab_plan(const kd_kl_problem& p, int64_t T, double budget) {
+BlockPlan slab_plan(const kd_kl_problem& p, int64_t T, double budget, bool all_tokens = false) {
   BlockPlan b{};
-  if (T <= p.V) {
+  if (all_tokens || T <= p.V) {
     b.Tb = T;
     int64_t vb_max = (int64_t)std::min<double>((double)p.V, std::floor(budget / (double)T));
     vb_max = std::max<int64_t>(vb_max, 256);
@@ -331,16 +345,18 @@ double rmw_bytes(const BlockPlan& b, int64_t T, const kd_kl_problem& p) {
 
 // own_teacher: the backward prepares the sorted teacher cache itself (sidx,
 // sp in its workspace); otherwise it reads the forward's.
-BwdPlan plan_backward(const kd_kl_problem& p, bool own_teacher = true) {
+// whole_dW: every dW tile comes from one launch (all tokens per vocabulary
+// slab, however many there are), as a dW rounded to bf16 on its way out needs.
+BwdPlan plan_backward(const kd_kl_problem& p, bool own_teacher = true, bool whole_dW = false) {
   BwdPlan b{};
   const int64_t T = std::max<int64_t>(p.T, 1);
   const double budget = (double)p.chunk * (double)p.V;  // gradient-of-logits elements
-  const BlockPlan slab = slab_plan(p, T, budget);
+  const BlockPlan slab = slab_plan(p, T, budget, whole_dW);
   const BlockPlan sq = square_plan(p, T, budget);
   const char* e2d = getenv("KDKL_BWD_2D");  // tuning: 1 / 0 forces the 2D / slab plan
   const bool two_d = e2d ? (e2d[0] == '1')
                          : (rmw_bytes(sq, T, p) <= 0.75 * rmw_bytes(slab, T, p));
-  const BlockPlan& bp = two_d ? sq : slab;
+  const BlockPlan& bp = two_d && !whole_dW ? sq : slab;
   b.Tb = bp.Tb;
   b.Vb = bp.Vb;
   b.n_tblocks = bp.n_tblocks;
@@ -737,86 +753,49 @@ kd_status kd_kl_forward_ex(const kd_kl_problem* prob, const kd_kl_options* opts,
                       workspace, workspace_bytes, stream);
 }
 
-static kd_status backward_impl(const kd_kl_problem* prob, const kd_kl_options* opts,
-                               const uint16_t* H, const uint16_t* W, const int32_t* topk_idx,
-                               const float* topk_logit, const uint8_t* mask, const float* lse,
-                               const float* lse1, float grad_loss, uint16_t* dH, float* dW,
-                               int accumulate_dW, void* workspace, size_t workspace_bytes,
-                               void* stream_ptr, const void* fwd_ws = nullptr,
-                               size_t fwd_ws_bytes = 0) {
-  const bool reuse = fwd_ws != nullptr;
-  // With a reused forward workspace the teacher cache is not read: stand-in
-  // non-null pointers pass the common checks.
-  kd_status st = validate_common(prob, H, W, reuse ? fwd_ws : topk_idx,
-                                 reuse ? fwd_ws : topk_logit, workspace);
-  if (st != KD_OK) return st;
-  if (reuse && !forward_matches(fwd_ws, fwd_ws_bytes, *prob, mask)) return KD_ERR_INVALID_ARG;
-  const bool mix = opts != nullptr;
-  if (mix && ((st = validate_options(prob, opts)) != KD_OK)) return st;
-  // temperature-1 logsumexp: needed when the CE term is on and tau != 1
-  if (mix && prob->T > 0 && !lse1 && opts->alpha < 1.0f && prob->temperature != 1.0f)
-    return KD_ERR_INVALID_ARG;
-  if (!aligned(lse1, 4)) return KD_ERR_ALIGNMENT;
-  if (!dW || (prob->T > 0 && (!lse || !dH))) return KD_ERR_INVALID_ARG;
-  if (!isfinite(grad_loss)) return KD_ERR_INVALID_ARG;
-  if (!aligned(dH, 16) || !aligned(dW, 16) || !aligned(lse, 4)) return KD_ERR_ALIGNMENT;
-  DeviceInfo di;
-  if ((st = device_info(&di)) != KD_OK) return st;
-  if ((st = get_encoder()) != KD_OK) return st;
-  const kd_kl_problem& p = *prob;
-  const BwdPlan b = plan_backward(p, !reuse);
-  if (workspace_bytes < b.total) return KD_ERR_WORKSPACE;
-  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+// What the blocks of a backward read and write (see kd_kl_backward).
+struct BackwardBlocks {
+  const kd_kl_options* opts;  // mixed loss, or null
+  const uint16_t *H, *W;
+  const uint16_t* Hc;  // the counted tokens' rows, or null: H's rows as they are
+  const int* rowmap;
+  const int32_t* sidx;
+  const float* sp;
+  const uint8_t* mask;
+  const float *lse, *lse1;
+  int* n_count;
+  float grad_loss;
+  const float* row_grad;  // upstream gradient per token, or null: grad_loss / N
+  float* dW;
+  uint16_t* dW16;  // bf16 dW instead of dW (one token block), or null
+  int accumulate_dW;
+};
 
+// The blocks' launches: recompute, dH (into the workspace's accumulator), dW.
+static kd_status backward_blocks(const kd_kl_problem& p, const BwdPlan& b, const BackwardBlocks& j,
+                                 void* workspace, int num_sms, cudaStream_t stream) {
   int* status = at<int>(workspace, 0);
-  // the counted-token total N: this call's own, or the forward's
-  int* n_count = reuse ? const_cast<int*>(static_cast<const int*>(fwd_ws)) + 1 : status + 1;
-  KD_CUDA(cudaMemsetAsync(workspace, 0, b.tl.off_sidx, stream));  // header and unit counters
   int* counters = static_schedule() ? nullptr : at<int>(workspace, b.off_ctr);
   int launch_no = 0;  // index of the next GEMM launch's counter
   auto next_counter = [&]() { return counters ? counters + launch_no++ : nullptr; };
-  if (p.T == 0) {
-    if (!accumulate_dW) KD_CUDA(cudaMemsetAsync(dW, 0, (size_t)p.V * p.d * 4, stream));
-    return KD_OK;
-  }
+  const bool mix = j.opts != nullptr;
   const int T = (int)p.T, K = p.K, V = (int)p.V, d = (int)p.d;
   const float inv_tau = 1.0f / p.temperature;
   const float cl2 = 1.4426950408889634f * inv_tau;
-  // The teacher side (sorted ids and p; with a mask, the compaction of the
-  // counted tokens): the forward workspace's, at the same offsets, or
-  // prepared here.
-  char* tws = reuse ? static_cast<char*>(const_cast<void*>(fwd_ws)) : static_cast<char*>(workspace);
-  const TeacherLayout tl = reuse ? teacher_layout(kHeaderBytes, p) : b.tl;
-  int32_t* sidx = at<int32_t>(tws, tl.off_sidx);
-  float* sp = at<float>(tws, tl.off_sp);
-  const bool compact = mask != nullptr;
-  int* rowmap = compact ? at<int>(tws, tl.off_rowmap) : nullptr;
-  int* invmap = compact ? at<int>(tws, tl.off_invmap) : nullptr;
-  uint16_t* Hc = at<uint16_t>(tws, tl.off_Hc);
-  const int64_t T_pad = round_up(T, 2 * BM);
   uint16_t* Gbuf = at<uint16_t>(workspace, b.off_G);
   float* dH_acc = at<float>(workspace, b.off_dH);
-
-  if (!reuse) {
-    if (compact) {
-      KD_CUDA(launch_mask_scan(mask, T, rowmap, invmap, n_count, stream));
-      KD_CUDA(launch_gather_rows(H, d, rowmap, n_count, T_pad, 2 * BM, Hc, di.num_sms, stream));
-    }
-    KD_CUDA(launch_teacher_prep(topk_idx, topk_logit, mask, mix ? opts->labels : nullptr, rowmap,
-                                T, K, V, inv_tau, sidx, sp, nullptr, n_count, status, stream));
-  }
-
   const bool pair = use_pair();
   const int tile_m = pair ? 2 * BM : BM;
-  const int procs = gemm_procs(di.num_sms, pair);
+  const int procs = gemm_procs(num_sms, pair);
   const int cta_per_proc = pair ? 2 : 1;
   // Rows of the token operand: the compacted counted tokens, or H itself.
-  const uint16_t* Hop = compact ? Hc : H;
-  const int64_t H_rows = compact ? T_pad : T;
+  const bool compact = j.Hc != nullptr;
+  const uint16_t* Hop = compact ? j.Hc : j.H;
+  const int64_t H_rows = compact ? round_up(p.T, 2 * BM) : p.T;
   CUtensorMap tmH_K, tmW_K, tmW_MN, tmH_MN;
   if (!encode_bf16_2d(&tmH_K, Hop, d, H_rows, d, BK, BM) ||
-      !encode_bf16_2d(&tmW_K, W, d, V, d, BK, pair ? LOGIT_BN / 2 : LOGIT_BN) ||
-      !encode_bf16_2d(&tmW_MN, W, d, V, d, 64, BK) ||
+      !encode_bf16_2d(&tmW_K, j.W, d, V, d, BK, pair ? LOGIT_BN / 2 : LOGIT_BN) ||
+      !encode_bf16_2d(&tmW_MN, j.W, d, V, d, 64, BK) ||
       !encode_bf16_2d(&tmH_MN, Hop, d, H_rows, d, 64, BK))
     return KD_ERR_CUDA;
 
@@ -858,15 +837,15 @@ static kd_status backward_impl(const kd_kl_problem* prob, const kd_kl_options* o
         sh.b_n0 = col0;
         sh.counter = next_counter();
         if (compact) {  // only the block's counted tokens
-          sh.dyn_rows = n_count;
+          sh.dyn_rows = j.n_count;
           sh.dyn_base = row0;
           sh.dyn_cap = rows;
           sh.dyn_dim = 0;
         }
         EpiParams ep{};
-        ep.rowmap = rowmap;
-        ep.sidx = sidx;
-        ep.sp = sp;
+        ep.rowmap = j.rowmap;
+        ep.sidx = j.sidx;
+        ep.sp = j.sp;
         ep.K = K;
         ep.T = T;
         ep.row0 = row0;
@@ -874,19 +853,20 @@ static kd_status backward_impl(const kd_kl_problem* prob, const kd_kl_options* o
         ep.col0 = col0;
         ep.cols = cols;
         ep.cl2 = cl2;
-        ep.lse = lse;
-        ep.mask = compact ? nullptr : mask;
-        ep.n_count = n_count;
-        ep.g_over_tau = grad_loss * inv_tau;
+        ep.lse = j.lse;
+        ep.mask = compact ? nullptr : j.mask;
+        ep.n_count = j.n_count;
+        ep.g_over_tau = j.grad_loss * inv_tau;
+        ep.row_grad = j.row_grad;
         ep.G = Gbuf;
         ep.ldg = b.Vb_pad;
         if (mix) {
-          const MixWeights mw = mix_weights(p, *opts);
-          ep.labels = opts->labels;
+          const MixWeights mw = mix_weights(p, *j.opts);
+          ep.labels = j.opts->labels;
           ep.same_tau = p.temperature == 1.0f ? 1 : 0;
-          ep.lse1 = lse1 ? lse1 : lse;
-          ep.kl_weight = grad_loss * mw.kl * inv_tau;
-          ep.ce_weight = grad_loss * mw.ce;
+          ep.lse1 = j.lse1 ? j.lse1 : j.lse;
+          ep.kl_weight = j.grad_loss * mw.kl * inv_tau;
+          ep.ce_weight = j.grad_loss * mw.ce;
         }
         const int grid = cta_per_proc * (int)std::min<int64_t>(sh.units, procs);
         if (log_plan() && vb == 0 && tb == 0) print_plan("bwd_grad", pair, procs, sh, grid);
@@ -913,7 +893,7 @@ static kd_status backward_impl(const kd_kl_problem* prob, const kd_kl_options* o
       sh_dh.b_k0 = col0;
       sh_dh.narrow_last = narrow_last;
       if (compact) {
-        sh_dh.dyn_rows = n_count;
+        sh_dh.dyn_rows = j.n_count;
         sh_dh.dyn_base = row0;
         sh_dh.dyn_cap = rows;
         sh_dh.dyn_dim = 0;  // M: the block's counted tokens
@@ -935,17 +915,20 @@ static kd_status backward_impl(const kd_kl_problem* prob, const kd_kl_options* o
       sh_dw.b_k0 = row0;
       sh_dw.narrow_last = narrow_last;
       if (compact) {
-        sh_dw.dyn_rows = n_count;
+        sh_dw.dyn_rows = j.n_count;
         sh_dw.dyn_base = row0;
         sh_dw.dyn_cap = rows;
         sh_dw.dyn_dim = 1;  // K: the block's counted tokens
       }
       EpiParams ep_dw{};
-      ep_dw.out = dW + (int64_t)col0 * d;
+      if (j.dW16)
+        ep_dw.out16 = j.dW16 + (int64_t)col0 * d;
+      else
+        ep_dw.out = j.dW + (int64_t)col0 * d;
       ep_dw.ldo = d;
       ep_dw.out_rows = cols;
       ep_dw.out_cols = d;
-      ep_dw.accumulate = (accumulate_dW || tb > 0) ? 1 : 0;
+      ep_dw.accumulate = (j.accumulate_dW || tb > 0) ? 1 : 0;
       // One launch pays only when both jobs are small (together at most two
       // waves of units): it saves a launch and a tail where each is a large
       // share of the work; the job with the longer units goes first. Otherwise
@@ -984,6 +967,89 @@ static kd_status backward_impl(const kd_kl_problem* prob, const kd_kl_options* o
       }
     }
   }
+  return KD_OK;
+}
+
+static kd_status backward_impl(const kd_kl_problem* prob, const kd_kl_options* opts,
+                               const uint16_t* H, const uint16_t* W, const int32_t* topk_idx,
+                               const float* topk_logit, const uint8_t* mask, const float* lse,
+                               const float* lse1, float grad_loss, uint16_t* dH, float* dW,
+                               int accumulate_dW, void* workspace, size_t workspace_bytes,
+                               void* stream_ptr, const void* fwd_ws = nullptr,
+                               size_t fwd_ws_bytes = 0) {
+  const bool reuse = fwd_ws != nullptr;
+  // With a reused forward workspace the teacher cache is not read: stand-in
+  // non-null pointers pass the common checks.
+  kd_status st = validate_common(prob, H, W, reuse ? fwd_ws : topk_idx,
+                                 reuse ? fwd_ws : topk_logit, workspace);
+  if (st != KD_OK) return st;
+  if (reuse && !forward_matches(fwd_ws, fwd_ws_bytes, *prob, mask)) return KD_ERR_INVALID_ARG;
+  const bool mix = opts != nullptr;
+  if (mix && ((st = validate_options(prob, opts)) != KD_OK)) return st;
+  // temperature-1 logsumexp: needed when the CE term is on and tau != 1
+  if (mix && prob->T > 0 && !lse1 && opts->alpha < 1.0f && prob->temperature != 1.0f)
+    return KD_ERR_INVALID_ARG;
+  if (!aligned(lse1, 4)) return KD_ERR_ALIGNMENT;
+  if (!dW || (prob->T > 0 && (!lse || !dH))) return KD_ERR_INVALID_ARG;
+  if (!isfinite(grad_loss)) return KD_ERR_INVALID_ARG;
+  if (!aligned(dH, 16) || !aligned(dW, 16) || !aligned(lse, 4)) return KD_ERR_ALIGNMENT;
+  DeviceInfo di;
+  if ((st = device_info(&di)) != KD_OK) return st;
+  if ((st = get_encoder()) != KD_OK) return st;
+  const kd_kl_problem& p = *prob;
+  const BwdPlan b = plan_backward(p, !reuse);
+  if (workspace_bytes < b.total) return KD_ERR_WORKSPACE;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+
+  int* status = at<int>(workspace, 0);
+  // the counted-token total N: this call's own, or the forward's
+  int* n_count = reuse ? const_cast<int*>(static_cast<const int*>(fwd_ws)) + 1 : status + 1;
+  KD_CUDA(cudaMemsetAsync(workspace, 0, b.tl.off_sidx, stream));  // header and unit counters
+  if (p.T == 0) {
+    if (!accumulate_dW) KD_CUDA(cudaMemsetAsync(dW, 0, (size_t)p.V * p.d * 4, stream));
+    return KD_OK;
+  }
+  const int T = (int)p.T, K = p.K, V = (int)p.V, d = (int)p.d;
+  const float inv_tau = 1.0f / p.temperature;
+  // The teacher side (sorted ids and p; with a mask, the compaction of the
+  // counted tokens): the forward workspace's, at the same offsets, or
+  // prepared here.
+  char* tws = reuse ? static_cast<char*>(const_cast<void*>(fwd_ws)) : static_cast<char*>(workspace);
+  const TeacherLayout tl = reuse ? teacher_layout(kHeaderBytes, p) : b.tl;
+  int32_t* sidx = at<int32_t>(tws, tl.off_sidx);
+  float* sp = at<float>(tws, tl.off_sp);
+  const bool compact = mask != nullptr;
+  int* rowmap = compact ? at<int>(tws, tl.off_rowmap) : nullptr;
+  int* invmap = compact ? at<int>(tws, tl.off_invmap) : nullptr;
+  uint16_t* Hc = at<uint16_t>(tws, tl.off_Hc);
+  const int64_t T_pad = round_up(T, 2 * BM);
+  float* dH_acc = at<float>(workspace, b.off_dH);
+
+  if (!reuse) {
+    if (compact) {
+      KD_CUDA(launch_mask_scan(mask, T, rowmap, invmap, n_count, stream));
+      KD_CUDA(launch_gather_rows(H, d, rowmap, n_count, T_pad, 2 * BM, Hc, di.num_sms, stream));
+    }
+    KD_CUDA(launch_teacher_prep(topk_idx, topk_logit, mask, mix ? opts->labels : nullptr, rowmap,
+                                T, K, V, inv_tau, sidx, sp, nullptr, n_count, status, stream));
+  }
+
+  BackwardBlocks bb{};
+  bb.opts = opts;
+  bb.H = H;
+  bb.W = W;
+  bb.Hc = compact ? Hc : nullptr;
+  bb.rowmap = rowmap;
+  bb.sidx = sidx;
+  bb.sp = sp;
+  bb.mask = mask;
+  bb.lse = lse;
+  bb.lse1 = lse1;
+  bb.n_count = n_count;
+  bb.grad_loss = grad_loss;
+  bb.dW = dW;
+  bb.accumulate_dW = accumulate_dW;
+  if ((st = backward_blocks(p, b, bb, workspace, di.num_sms, stream)) != KD_OK) return st;
   // dH rows back to the callers' tokens; masked rows are exact zeros
   KD_CUDA(launch_f32_to_bf16(dH_acc, dH, (long long)p.T * p.d, d, invmap, di.num_sms, stream));
   return KD_OK;
@@ -1174,6 +1240,183 @@ kd_status kd_lmhead_topk(const kd_topk_problem* prob, const uint16_t* H, const u
   KD_CUDA(launch_topk_merge(ep.unit_val, ep.unit_id, ep.unit_cnt, ep.row_key, f.nsplit, T, K,
                             topk_idx,
                             topk_logit, stream));
+  return KD_OK;
+}
+
+// ---- token log-probabilities: the KL path with a teacher of one entry per
+// token (its own id, weight 1), whose "dot" is the token's logit.
+
+static bool logprob_problem(const kd_logprob_problem* p, kd_kl_problem* out) {
+  if (!p) return false;
+  *out = kd_kl_problem{p->T, p->d, p->V, 1, p->temperature, p->chunk};
+  return problem_ok(out);
+}
+
+static kd_status logprob_validate(const kd_logprob_problem* p, const void* H, const void* W,
+                                  const void* ids, const void* workspace) {
+  if (!p) return KD_ERR_INVALID_ARG;
+  const kd_kl_problem q{p->T, p->d, p->V, 1, p->temperature, p->chunk};
+  return validate_common(&q, H, W, ids, ids, workspace);
+}
+
+// Vocabulary tiles per unit of the forward: 8 as in the KL forward when the
+// tiles fill the processors many times over, fewer when they do not (one tile
+// of tokens against a vocabulary of 786 tiles is 98 units of 8 for 76 pairs,
+// two rounds of which the second is a third full). Eight tiles need 16 units
+// for each processor.
+static int logprob_split_tiles(const kd_kl_problem& p, bool pair, int procs) {
+  const int64_t tiles = ceil_div(p.V, LOGIT_BN) *
+                        std::max<int64_t>(1, ceil_div(p.T, pair ? 2 * BM : BM));
+  return (int)std::max<int64_t>(1, std::min<int64_t>(8, tiles / (16 * (int64_t)procs)));
+}
+
+static FwdPlan plan_logprob(const kd_kl_problem& p, int num_sms, bool pair, int procs) {
+  return plan_forward(p, num_sms, pair, procs, false, logprob_split_tiles(p, pair, procs));
+}
+
+size_t kd_logprob_workspace_size(const kd_logprob_problem* prob, int which) {
+  kd_kl_problem p;
+  if (!logprob_problem(prob, &p)) return 0;
+  if (which == 1) return plan_backward(p, true, prob->dw_bf16 != 0).total;
+  if (which != 0) return 0;
+  DeviceInfo di;
+  const int sms = (device_info(&di) == KD_OK) ? di.num_sms : 160;
+  size_t total = plan_logprob(p, sms, false, sms).total;
+  for (int procs = 1; procs <= sms / 2; ++procs)
+    total = std::max(total, plan_logprob(p, sms, true, procs).total);
+  return total;
+}
+
+kd_status kd_logprob_forward(const kd_logprob_problem* prob, const uint16_t* H, const uint16_t* W,
+                             const int32_t* ids, const uint8_t* mask, float* logp, float* lse,
+                             void* workspace, size_t workspace_bytes, void* stream_ptr) {
+  kd_status st = logprob_validate(prob, H, W, ids, workspace);
+  if (st != KD_OK) return st;
+  kd_kl_problem p;
+  logprob_problem(prob, &p);
+  if (p.T > 0 && (!logp || !lse)) return KD_ERR_INVALID_ARG;
+  if (!aligned(logp, 4) || !aligned(lse, 4)) return KD_ERR_ALIGNMENT;
+  DeviceInfo di;
+  if ((st = device_info(&di)) != KD_OK) return st;
+  if ((st = get_encoder()) != KD_OK) return st;
+  const bool pair = use_pair();
+  const FwdPlan f = plan_logprob(p, di.num_sms, pair, gemm_procs(di.num_sms, pair));
+  if (workspace_bytes < f.total) return KD_ERR_WORKSPACE;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  forget_forward(workspace);
+  int* status = at<int>(workspace, 0);
+  int* n_count = status + 1;
+  KD_CUDA(cudaMemsetAsync(workspace, 0, kHeaderBytes, stream));
+  if (p.T == 0) return KD_OK;
+  const int T = (int)p.T, V = (int)p.V, d = (int)p.d;
+  const float inv_tau = 1.0f / p.temperature;
+  const float cl2 = 1.4426950408889634f * inv_tau;
+  int32_t* sidx = at<int32_t>(workspace, f.tl.off_sidx);
+  float* sp = at<float>(workspace, f.tl.off_sp);
+  const bool compact = mask != nullptr;
+  int* rowmap = compact ? at<int>(workspace, f.tl.off_rowmap) : nullptr;
+  int* invmap = compact ? at<int>(workspace, f.tl.off_invmap) : nullptr;
+  uint16_t* Hc = at<uint16_t>(workspace, f.tl.off_Hc);
+  const int64_t T_pad = round_up(T, 2 * BM);
+  if (compact) {
+    KD_CUDA(launch_mask_scan(mask, T, rowmap, invmap, n_count, stream));
+    KD_CUDA(launch_gather_rows(H, d, rowmap, n_count, T_pad, 2 * BM, Hc, di.num_sms, stream));
+  }
+  KD_CUDA(launch_label_prep(ids, rowmap, n_count, T, V, sidx, sp, status, stream));
+  CUtensorMap tmH, tmW;
+  if (!encode_bf16_2d(&tmH, compact ? Hc : H, d, compact ? T_pad : T, d, BK, BM) ||
+      !encode_bf16_2d(&tmW, W, d, V, d, BK, pair ? LOGIT_BN / 2 : LOGIT_BN))
+    return KD_ERR_CUDA;
+  GemmShape sh{};
+  sh.inject_stall = inject_stall_from_env();
+  sh.m_tiles = f.m_tiles;
+  sh.n_tiles = f.n_tiles;
+  sh.nsplit = f.nsplit;
+  sh.group_m = f.group_m;
+  sh.units = f.m_tiles * f.nsplit;
+  sh.k_blocks = (int)ceil_div(d, BK);
+  sh.counter = static_schedule() ? nullptr : status + kHeaderCounter0;
+  if (compact) {
+    sh.dyn_rows = n_count;
+    sh.dyn_cap = T;
+  }
+  EpiParams ep{};
+  ep.rowmap = rowmap;
+  ep.sidx = sidx;
+  ep.sp = sp;
+  ep.K = 1;
+  ep.T = T;
+  ep.rows = T;
+  ep.cols = V;
+  ep.cl2 = cl2;
+  ep.pm = at<float>(workspace, f.off_pm);
+  ep.ps = at<float>(workspace, f.off_ps);
+  ep.pd = at<float>(workspace, f.off_pd);
+  if (log_plan()) print_plan("logprob", pair, gemm_procs(di.num_sms, pair), sh, f.grid);
+  KD_CUDA(launch_gemm(GEMM_FWD_LSE, LOGIT_BN, pair, tmH, tmW, sh, ep, status, f.grid, stream));
+  KD_CUDA(launch_logp_combine(ep.pm, ep.ps, ep.pd, f.nsplit, T, invmap, cl2, inv_tau, logp, lse,
+                              stream));
+  return KD_OK;
+}
+
+kd_status kd_logprob_backward(const kd_logprob_problem* prob, const uint16_t* H, const uint16_t* W,
+                              const int32_t* ids, const float* lse, const float* grad_logp,
+                              uint16_t* dH, void* dW, int accumulate_dW, void* workspace,
+                              size_t workspace_bytes, void* stream_ptr) {
+  kd_status st = logprob_validate(prob, H, W, ids, workspace);
+  if (st != KD_OK) return st;
+  kd_kl_problem p;
+  logprob_problem(prob, &p);
+  const bool bf16 = prob->dw_bf16 != 0;
+  if (!dW || (p.T > 0 && (!lse || !grad_logp || !dH))) return KD_ERR_INVALID_ARG;
+  if (bf16 && accumulate_dW) return KD_ERR_INVALID_ARG;
+  if (!aligned(dH, 16) || !aligned(dW, 16) || !aligned(lse, 4) || !aligned(grad_logp, 4))
+    return KD_ERR_ALIGNMENT;
+  DeviceInfo di;
+  if ((st = device_info(&di)) != KD_OK) return st;
+  if ((st = get_encoder()) != KD_OK) return st;
+  const BwdPlan b = plan_backward(p, true, bf16);
+  if (workspace_bytes < b.total) return KD_ERR_WORKSPACE;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  forget_forward(workspace);
+  int* status = at<int>(workspace, 0);
+  int* n_count = status + 1;
+  KD_CUDA(cudaMemsetAsync(workspace, 0, b.tl.off_sidx, stream));  // header and unit counters
+  if (p.T == 0) {
+    if (!accumulate_dW)
+      KD_CUDA(cudaMemsetAsync(dW, 0, (size_t)p.V * p.d * (bf16 ? 2 : 4), stream));
+    return KD_OK;
+  }
+  const int T = (int)p.T, V = (int)p.V, d = (int)p.d;
+  int32_t* sidx = at<int32_t>(workspace, b.tl.off_sidx);
+  float* sp = at<float>(workspace, b.tl.off_sp);
+  int* rowmap = at<int>(workspace, b.tl.off_rowmap);
+  int* invmap = at<int>(workspace, b.tl.off_invmap);
+  uint16_t* Hc = at<uint16_t>(workspace, b.tl.off_Hc);
+  // Only the tokens with a gradient, as the other calls do with a mask.
+  KD_CUDA(launch_grad_scan(grad_logp, T, rowmap, invmap, n_count, stream));
+  KD_CUDA(launch_gather_rows(H, d, rowmap, n_count, round_up(T, 2 * BM), 2 * BM, Hc, di.num_sms,
+                             stream));
+  KD_CUDA(launch_label_prep(ids, rowmap, n_count, T, V, sidx, sp, status, stream));
+  BackwardBlocks bb{};
+  bb.H = H;
+  bb.W = W;
+  bb.Hc = Hc;
+  bb.rowmap = rowmap;
+  bb.sidx = sidx;
+  bb.sp = sp;
+  bb.lse = lse;
+  bb.n_count = n_count;
+  bb.grad_loss = 1.f;
+  bb.row_grad = grad_logp;
+  if (bf16)
+    bb.dW16 = static_cast<uint16_t*>(dW);
+  else
+    bb.dW = static_cast<float*>(dW);
+  bb.accumulate_dW = accumulate_dW;
+  if ((st = backward_blocks(p, b, bb, workspace, di.num_sms, stream)) != KD_OK) return st;
+  KD_CUDA(launch_f32_to_bf16(at<float>(workspace, b.off_dH), dH, (long long)p.T * p.d, d, invmap,
+                             di.num_sms, stream));
   return KD_OK;
 }
 

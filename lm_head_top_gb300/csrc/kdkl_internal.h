@@ -145,4 +145,75 @@ cudaError_t launch_gemm_dw_dh(bool pair, bool dh_first, const CUtensorMap& tmG_M
                               const CUtensorMap& tmW_MN, const GemmShape& sh_dh,
                               const EpiParams& ep_dh, int* status, int grid, cudaStream_t stream);
 
+// kernels_small.cu, for the token log-probabilities
+// Compaction of the tokens whose gradient is not zero (NaN included).
+cudaError_t launch_grad_scan(const float* grad, int T, int* rowmap, int* invmap, int* n_count,
+                             cudaStream_t stream);
+// Row r's id and weight 1, as a teacher row of one entry; checks the id.
+cudaError_t launch_label_prep(const int32_t* ids, const int* rowmap, const int* n_count, int T,
+                              int V, int32_t* sidx, float* sp, int* status, cudaStream_t stream);
+cudaError_t launch_logp_combine(const float* pm, const float* ps, const float* pd, int nsplit,
+                                int T, const int* invmap, float cl2, float inv_tau, float* logp,
+                                float* lse, cudaStream_t stream);
+
+// kernels_policy.cu
+struct PolicyArgs {
+  const float *logp, *old_logp, *ref_logp, *advantages;
+  const uint8_t* mask;
+  const int32_t* cu;
+  int T, S, vec, reduction, adv_per_seq, count_here, dual;
+  float inv_norm, kl_coef, grad_loss;
+  float r_low, r_high, r_dual;                                       // clipped ratios
+  float low_hi, low_lo, high_hi, high_lo, dual_hi, dual_lo;          // borders of logp - old_logp
+  int* n_count;        // [0] counted tokens, [1] sequences that have any
+  int* n_seq;          // [S] counted tokens of each sequence
+  int* ticket;         // [2] blocks done (loss, count)
+  double* block_part;  // [blocks, 3]
+  float *loss, *stats, *grad;
+};
+struct PrefArgs {
+  const float *logp, *ref_logp;
+  const uint8_t* mask;
+  const int32_t* cu;
+  int T, P, vec, kind, average, halves;
+  double beta, label_smoothing, margin, grad_loss;
+  double* slot_sum;   // [blocks + 2P]
+  int* slot_n;        // [blocks + 2P]
+  double* pair_loss;  // [P]
+  float* coef;        // [2P] gradient of a sequence's counted tokens
+  int* ticket;
+  float *loss, *rewards, *grad;
+};
+// Masks of up to so many tokens are counted by every block of the loss kernel for itself.
+constexpr int kPolicyCountHere = 32768;
+int seq_blocks(int T);
+cudaError_t launch_policy_loss(const PolicyArgs& a, int* status, cudaStream_t stream);
+cudaError_t launch_pref_loss(const PrefArgs& a, int* status, cudaStream_t stream);
+
+// kernels_adamw.cu
+struct AdamTensor {
+  void* param;
+  const void* grad;
+  void *exp_avg, *exp_avg_sq;
+  uint16_t* copy;
+  float *m_scale, *v_scale;
+  long long n;
+  int block0;  // first thread block of this tensor in its launch
+  int decay;
+  int vec;     // every pointer allows 16-byte accesses of 8 elements
+  int pad;
+};
+struct AdamScalars {
+  float b1, one_b1, b2, one_b2, inv_root_bc2, eps, step, keep, grad_scale;
+  const float* grad_scale_dev;
+};
+constexpr int ADAMW_SHORT_LIST = 32;
+constexpr int ADAMW_LIST = 384;  // 30 KB of the 32,764 bytes a kernel's parameters may take
+int adamw_blocks(long long n);
+cudaError_t launch_adamw(const AdamTensor* t, int n, int blocks, bool param_bf16, bool grad_bf16,
+                         bool state8, const AdamScalars& s, cudaStream_t stream);
+
+// kdkl_api.cu: the current device's SM count; KD_OK, KD_ERR_CUDA or KD_ERR_UNSUPPORTED.
+int current_device(int* num_sms);
+
 }  // namespace kdkl

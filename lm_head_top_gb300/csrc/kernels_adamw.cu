@@ -1,0 +1,310 @@
+// AdamW over a list of tensors in one launch, states in 32 or in 8 bits.
+//
+//   g' = g * grad_scale            m' = b1 m + (1 - b1) g'
+//   v' = b2 v + (1 - b2) g'^2      p' = p (1 - lr wd) - lr/(1-b1^t) * m' / (sqrt(v') / sqrt(1-b2^t) + eps)
+//
+// Every product, sum, root and quotient is rounded to fp32 by itself, in the
+// order written (no contraction into fused multiply-adds): the results are
+// those of the elementwise formula, bit for bit, whichever path computes them.
+//
+// 8-bit states: m and the root r = sqrt(v) are held in e4m3, 256 consecutive
+// elements sharing one fp32 power of two, the least with which the block's
+// largest magnitude stays within 463.04 (which rounds to e4m3's largest, 448). The root, not v: e4m3 spans 2^17.8 from
+// its smallest step to its largest value, which as a root spans 2^35 of v. A
+// root that is not zero is never stored as zero (it would divide by eps
+// alone). This step's update uses the 32-bit m' and sqrt(v'); only what is
+// kept for the next step is rounded to 8 bits (m to a relative 2^-4, the root
+// likewise: what the user chose when asking for 8-bit states). A power of two
+// as the scale makes scaling exact, so e4m3 is the only rounding.
+//
+// What bounds it: DRAM. Read g, p, m, v and write p, m, v (and the bf16 copy):
+// 30 bytes per element with fp32 gradients, 32-bit states and a copy.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <stdint.h>
+
+#include "kdkl_internal.h"
+#include "tc_primitives.cuh"
+
+namespace kdkl {
+
+namespace {
+
+constexpr int ADAM_THREADS = 256;
+constexpr int ADAM_VEC = 8;      // consecutive elements per thread; a warp covers one scale block
+constexpr int ADAM_BLOCK = 256;  // elements per scale
+constexpr int ADAM_PASSES = 4;
+constexpr int ADAM_CHUNK = ADAM_THREADS * ADAM_VEC * ADAM_PASSES;  // elements per thread block
+
+static_assert(ADAM_VEC * 32 == ADAM_BLOCK, "a warp's pass is one scale block");
+
+// The tensors of one launch travel as a kernel parameter: no table in device
+// memory to build, upload or keep in step with the tensors.
+template <int CAP>
+struct AdamTable {
+  AdamTensor t[CAP];
+  int n;
+};
+
+struct Vec8 {
+  float x[ADAM_VEC];
+};
+
+__device__ __forceinline__ float bf16_to_f32(uint16_t v) {
+  return __uint_as_float((uint32_t)v << 16);
+}
+__device__ __forceinline__ uint16_t f32_to_bf16(float v) {
+  return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+
+// Eight consecutive elements from index i; those at or past n read as zero.
+__device__ __forceinline__ Vec8 load8(const float* p, long long i, long long n, bool vec) {
+  Vec8 r;
+  if (vec && i + ADAM_VEC <= n) {
+    const float4 a = __ldcs(reinterpret_cast<const float4*>(p + i));
+    const float4 b = __ldcs(reinterpret_cast<const float4*>(p + i) + 1);
+    r.x[0] = a.x; r.x[1] = a.y; r.x[2] = a.z; r.x[3] = a.w;
+    r.x[4] = b.x; r.x[5] = b.y; r.x[6] = b.z; r.x[7] = b.w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < ADAM_VEC; ++j) r.x[j] = i + j < n ? p[i + j] : 0.f;
+  }
+  return r;
+}
+
+__device__ __forceinline__ Vec8 load8(const uint16_t* p, long long i, long long n, bool vec) {
+  Vec8 r;
+  if (vec && i + ADAM_VEC <= n) {
+    const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p + i));
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      r.x[2 * j] = __uint_as_float(w[j] << 16);
+      r.x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < ADAM_VEC; ++j) r.x[j] = i + j < n ? bf16_to_f32(p[i + j]) : 0.f;
+  }
+  return r;
+}
+
+__device__ __forceinline__ void store8(float* p, long long i, long long n, bool vec,
+                                       const Vec8& r) {
+  if (vec && i + ADAM_VEC <= n) {
+    __stcs(reinterpret_cast<float4*>(p + i), make_float4(r.x[0], r.x[1], r.x[2], r.x[3]));
+    __stcs(reinterpret_cast<float4*>(p + i) + 1, make_float4(r.x[4], r.x[5], r.x[6], r.x[7]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < ADAM_VEC; ++j)
+      if (i + j < n) p[i + j] = r.x[j];
+  }
+}
+
+__device__ __forceinline__ void store8(uint16_t* p, long long i, long long n, bool vec,
+                                       const Vec8& r) {
+  if (vec && i + ADAM_VEC <= n) {
+    uint4 w;
+    w.x = pack_bf16x2(r.x[0], r.x[1]);
+    w.y = pack_bf16x2(r.x[2], r.x[3]);
+    w.z = pack_bf16x2(r.x[4], r.x[5]);
+    w.w = pack_bf16x2(r.x[6], r.x[7]);
+    __stcs(reinterpret_cast<uint4*>(p + i), w);
+  } else {
+#pragma unroll
+    for (int j = 0; j < ADAM_VEC; ++j)
+      if (i + j < n) p[i + j] = f32_to_bf16(r.x[j]);
+  }
+}
+
+// Eight e4m3 codes from index i as their values; codes past n read as zero.
+__device__ __forceinline__ Vec8 load_e4m3(const uint8_t* p, long long i, long long n, bool vec) {
+  uint32_t w[2] = {0u, 0u};
+  if (vec && i + ADAM_VEC <= n) {
+    const uint2 a = __ldcs(reinterpret_cast<const uint2*>(p + i));
+    w[0] = a.x;
+    w[1] = a.y;
+  } else {
+#pragma unroll
+    for (int j = 0; j < ADAM_VEC; ++j)
+      if (i + j < n) w[j >> 2] |= (uint32_t)p[i + j] << (8 * (j & 3));
+  }
+  Vec8 r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const __nv_fp8x2_storage_t two = (__nv_fp8x2_storage_t)(w[j >> 1] >> (16 * (j & 1)));
+    const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3)));
+    r.x[2 * j] = f.x;
+    r.x[2 * j + 1] = f.y;
+  }
+  return r;
+}
+
+__device__ __forceinline__ void store_e4m3(uint8_t* p, long long i, long long n, bool vec,
+                                           const Vec8& r) {
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const __nv_fp8x2_storage_t two = __nv_cvt_float2_to_fp8x2(
+        make_float2(r.x[2 * j], r.x[2 * j + 1]), __NV_SATFINITE, __NV_E4M3);
+    w[j >> 1] |= (uint32_t)two << (16 * (j & 1));
+  }
+  if (vec && i + ADAM_VEC <= n) {
+    __stcs(reinterpret_cast<uint2*>(p + i), make_uint2(w[0], w[1]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < ADAM_VEC; ++j)
+      if (i + j < n) p[i + j] = (uint8_t)(w[j >> 2] >> (8 * (j & 3)));
+  }
+}
+
+// The scale block's largest finite magnitude over the warp, then the least
+// power of two (not below 2^-126) that keeps it within 512 * 0.904383 = 463.04,
+// which rounds to 448. (448 itself, or any border of few bits, is met exactly by
+// sums of 8-bit states and bf16 gradients, and the last bit of such a sum would
+// then set the scale.) An all-zero block gets 1.
+__device__ __forceinline__ float block_scale(const Vec8& r) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < ADAM_VEC; ++j) {
+    const uint32_t a = __float_as_uint(r.x[j]) & 0x7fffffffu;
+    top = max(top, a < 0x7f800000u ? a : 0u);  // infinities and NaN do not set the scale
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (top == 0u) return 1.f;
+  const float half = __uint_as_float((top & 0x7fffffu) | 0x3f000000u);  // in [0.5, 1)
+  const int e = (int)(top >> 23) - 126 - 9 + (half > 0.904383f ? 1 : 0);
+  return __uint_as_float((uint32_t)(max(e, -126) + 127) << 23);
+}
+
+__device__ __forceinline__ float pow2_inverse(float s) {  // s = 2^e, -126 <= e <= 120
+  return __uint_as_float(0x7f000000u - __float_as_uint(s));
+}
+
+// Finite values in units of the block's scale; infinities become NaN, which
+// e4m3 can hold and infinities it cannot.
+__device__ __forceinline__ Vec8 in_units(const Vec8& r, float scale) {
+  const float inv = pow2_inverse(scale);
+  Vec8 q;
+#pragma unroll
+  for (int j = 0; j < ADAM_VEC; ++j) {
+    const float y = __fmul_rn(r.x[j], inv);
+    q.x[j] = fabsf(r.x[j]) < INFINITY ? y : __uint_as_float(0x7fffffffu);
+  }
+  return q;
+}
+
+template <typename P, typename G, bool STATE8, int CAP>
+__global__ void __launch_bounds__(ADAM_THREADS)
+    adamw_kernel(const __grid_constant__ AdamTable<CAP> table, const AdamScalars s) {
+  // The tensor of this block: the last one whose first block is not past it.
+  int lo = 0, hi = table.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (table.t[mid].block0 <= (int)blockIdx.x) lo = mid; else hi = mid - 1;
+  }
+  const AdamTensor& t = table.t[lo];
+  const long long n = t.n;
+  const bool vec = t.vec != 0;
+  const float keep = t.decay ? s.keep : 1.f;
+  const float gs = s.grad_scale_dev ? __fmul_rn(s.grad_scale, __ldg(s.grad_scale_dev))
+                                    : s.grad_scale;
+  const long long base = (long long)((int)blockIdx.x - t.block0) * ADAM_CHUNK;
+#pragma unroll 1
+  for (int k = 0; k < ADAM_PASSES; ++k) {
+    const long long first = base + (long long)k * (ADAM_THREADS * ADAM_VEC) +
+                            (threadIdx.x & ~31) * ADAM_VEC;  // the warp's first element
+    if (first >= n) return;                                  // the whole warp
+    const long long i = first + (threadIdx.x & 31) * ADAM_VEC;
+    const Vec8 g = load8(static_cast<const G*>(t.grad), i, n, vec);
+    Vec8 p = load8(static_cast<const P*>(t.param), i, n, vec);
+    Vec8 m, v;
+    if (STATE8) {
+      m = load_e4m3(static_cast<const uint8_t*>(t.exp_avg), i, n, vec);
+      v = load_e4m3(static_cast<const uint8_t*>(t.exp_avg_sq), i, n, vec);
+      const float ms = t.m_scale[first / ADAM_BLOCK], vs = t.v_scale[first / ADAM_BLOCK];
+#pragma unroll
+      for (int j = 0; j < ADAM_VEC; ++j) {
+        m.x[j] = __fmul_rn(m.x[j], ms);
+        const float r = __fmul_rn(v.x[j], vs);
+        v.x[j] = __fmul_rn(r, r);
+      }
+    } else {
+      m = load8(static_cast<const float*>(t.exp_avg), i, n, vec);
+      v = load8(static_cast<const float*>(t.exp_avg_sq), i, n, vec);
+    }
+    Vec8 root;
+#pragma unroll
+    for (int j = 0; j < ADAM_VEC; ++j) {
+      const float gj = __fmul_rn(g.x[j], gs);
+      m.x[j] = __fadd_rn(__fmul_rn(m.x[j], s.b1), __fmul_rn(gj, s.one_b1));
+      v.x[j] = __fadd_rn(__fmul_rn(v.x[j], s.b2), __fmul_rn(__fmul_rn(gj, gj), s.one_b2));
+      root.x[j] = __fsqrt_rn(v.x[j]);
+      const float den = __fadd_rn(__fmul_rn(root.x[j], s.inv_root_bc2), s.eps);
+      const float u = __fmul_rn(__fdiv_rn(m.x[j], den), s.step);
+      p.x[j] = __fsub_rn(__fmul_rn(p.x[j], keep), u);
+    }
+    store8(static_cast<P*>(t.param), i, n, vec, p);
+    if (t.copy) store8(t.copy, i, n, vec, p);
+    if (STATE8) {
+      // Elements past n are zero here and set no scale.
+      const float ms = block_scale(m), vs = block_scale(root);
+      const Vec8 qm = in_units(m, ms);
+      Vec8 qr = in_units(root, vs);
+#pragma unroll
+      for (int j = 0; j < ADAM_VEC; ++j)
+        if (root.x[j] > 0.f && root.x[j] < INFINITY)
+          qr.x[j] = fmaxf(qr.x[j], 0.001953125f);  // 2^-9, e4m3's least step
+      store_e4m3(static_cast<uint8_t*>(t.exp_avg), i, n, vec, qm);
+      store_e4m3(static_cast<uint8_t*>(t.exp_avg_sq), i, n, vec, qr);
+      if ((threadIdx.x & 31) == 0) {
+        t.m_scale[first / ADAM_BLOCK] = ms;
+        t.v_scale[first / ADAM_BLOCK] = vs;
+      }
+    } else {
+      store8(static_cast<float*>(t.exp_avg), i, n, vec, m);
+      store8(static_cast<float*>(t.exp_avg_sq), i, n, vec, v);
+    }
+  }
+}
+
+template <typename P, typename G, bool STATE8, int CAP>
+cudaError_t launch_table(const AdamTensor* t, int n, int blocks, const AdamScalars& s,
+                         cudaStream_t stream) {
+  AdamTable<CAP> table;
+  for (int i = 0; i < n; ++i) table.t[i] = t[i];
+  table.n = n;
+  return launch_kernel("adamw", adamw_kernel<P, G, STATE8, CAP>, dim3((unsigned)blocks),
+                       dim3(ADAM_THREADS), 0, stream, table, s);
+}
+
+template <typename P, typename G, bool STATE8>
+cudaError_t launch_typed(const AdamTensor* t, int n, int blocks, const AdamScalars& s,
+                         cudaStream_t stream) {
+  // A short list takes the short parameter.
+  if (n <= ADAMW_SHORT_LIST)
+    return launch_table<P, G, STATE8, ADAMW_SHORT_LIST>(t, n, blocks, s, stream);
+  return launch_table<P, G, STATE8, ADAMW_LIST>(t, n, blocks, s, stream);
+}
+
+}  // namespace
+
+int adamw_blocks(long long n) { return (int)((n + ADAM_CHUNK - 1) / ADAM_CHUNK); }
+
+cudaError_t launch_adamw(const AdamTensor* t, int n, int blocks, bool param_bf16, bool grad_bf16,
+                         bool state8, const AdamScalars& s, cudaStream_t stream) {
+  const int kind = (param_bf16 ? 4 : 0) | (grad_bf16 ? 2 : 0) | (state8 ? 1 : 0);
+  switch (kind) {
+    case 0: return launch_typed<float, float, false>(t, n, blocks, s, stream);
+    case 1: return launch_typed<float, float, true>(t, n, blocks, s, stream);
+    case 2: return launch_typed<float, uint16_t, false>(t, n, blocks, s, stream);
+    case 3: return launch_typed<float, uint16_t, true>(t, n, blocks, s, stream);
+    case 4: return launch_typed<uint16_t, float, false>(t, n, blocks, s, stream);
+    case 5: return launch_typed<uint16_t, float, true>(t, n, blocks, s, stream);
+    case 6: return launch_typed<uint16_t, uint16_t, false>(t, n, blocks, s, stream);
+    default: return launch_typed<uint16_t, uint16_t, true>(t, n, blocks, s, stream);
+  }
+}
+
+}  // namespace kdkl

@@ -430,9 +430,11 @@ __global__ void f32_to_bf16_kernel(const float4* __restrict__ in, uint2* __restr
 // chunks of a tile, counts them with ballots (lane j keeps chunk j's count),
 // a block scan gives each chunk its first row, and a second pass writes the
 // maps. Loads and invmap stores are coalesced 32-token pieces.
+// M: the mask's bytes, or the tokens' fp32 gradients (NaN counts).
 constexpr int SCAN_THREADS = 1024;
+template <typename M>
 __global__ void __launch_bounds__(SCAN_THREADS)
-    mask_scan_kernel(const uint8_t* __restrict__ mask, int T, int* __restrict__ rowmap,
+    mask_scan_kernel(const M* __restrict__ mask, int T, int* __restrict__ rowmap,
                      int* __restrict__ invmap, int* __restrict__ n_count) {
   __shared__ int warp_base[SCAN_THREADS / 32];
   __shared__ int tile_total;
@@ -445,7 +447,7 @@ __global__ void __launch_bounds__(SCAN_THREADS)
     int my_count = 0;                                     // chunk `lane` of this warp
     for (int j = 0; j < 32; ++j) {
       const long long t = w0 + (long long)j * 32 + lane;
-      const bool on = t < T && mask[t] != 0;
+      const bool on = t < T && mask[t] != (M)0;
       const int c = __popc(__ballot_sync(0xffffffffu, on));
       if (lane == j) my_count = c;
     }
@@ -472,7 +474,7 @@ __global__ void __launch_bounds__(SCAN_THREADS)
     const int chunk_first = base + warp_base[warp] + incl - my_count;  // chunk `lane`'s first row
     for (int j = 0; j < 32; ++j) {
       const long long t = w0 + (long long)j * 32 + lane;
-      const bool on = t < T && mask[t] != 0;
+      const bool on = t < T && mask[t] != (M)0;
       const uint32_t b = __ballot_sync(0xffffffffu, on);
       const int first = __shfl_sync(0xffffffffu, chunk_first, j);
       if (t < T) {
@@ -485,6 +487,68 @@ __global__ void __launch_bounds__(SCAN_THREADS)
     __syncthreads();  // warp_base and tile_total are rewritten by the next tile
   }
   if (threadIdx.x == 0) *n_count = base;
+}
+
+// Rows of one teacher entry each: the token's own id with weight 1, so that
+// the GEMM epilogues pick z at that id and subtract its one-hot.
+__global__ void label_prep_kernel(const int32_t* __restrict__ ids, const int* __restrict__ rowmap,
+                                  const int* __restrict__ n_count, int T, int V,
+                                  int32_t* __restrict__ sidx, float* __restrict__ sp,
+                                  int* __restrict__ status) {
+  const int r = blockIdx.x * blockDim.x + threadIdx.x;
+  if (r >= (rowmap ? min(*n_count, T) : T)) return;
+  const int id = ids[rowmap ? rowmap[r] : r];
+  if (id < 0 || id >= V) record_error(status, DEV_ERR_INDEX_RANGE);
+  sidx[r] = id;
+  sp[r] = 1.f;
+}
+
+// Per token, the vocabulary splits' partials (max, sum of exponentials, the
+// logit at the token's id) to lse and logp = (z - max)/tau - log(sum): the
+// maximum cancels before it is scaled. TOK tokens per block, 256 / TOK threads
+// on each one's splits, merged in a fixed order. invmap as in lse_combine.
+template <int TOK>
+__global__ void __launch_bounds__(COMBINE_THREADS)
+    logp_combine_kernel(const float* __restrict__ pm, const float* __restrict__ ps,
+                        const float* __restrict__ pd, int nsplit, int T,
+                        const int* __restrict__ invmap, float cl2, float inv_tau,
+                        float* __restrict__ logp, float* __restrict__ lse) {
+  constexpr int STRANDS = COMBINE_THREADS / TOK;
+  const int i = threadIdx.x % TOK, w = threadIdx.x / TOK;
+  const int t = blockIdx.x * TOK + i;
+  const int r = t < T ? (invmap ? invmap[t] : t) : -1;
+  float M = -INFINITY, S = 0.f, D = 0.f;
+  if (r >= 0) {
+#pragma unroll 4
+    for (int s = w; s < nsplit; s += STRANDS) {
+      const long long o = (long long)s * T + r;
+      const float m = pm[o];
+      const float nm = fmaxf(M, m);
+      S = S * rescale2(M, nm, cl2) + ps[o] * rescale2(m, nm, cl2);
+      D += pd[o];
+      M = nm;
+    }
+  }
+  __shared__ float part[3][STRANDS][TOK];
+  part[0][w][i] = M;
+  part[1][w][i] = S;
+  part[2][w][i] = D;
+  for (int half = STRANDS / 2; half > 0; half >>= 1) {
+    __syncthreads();
+    if (w < half) {
+      const float a = part[0][w][i], b = part[0][w + half][i];
+      const float m = fmaxf(a, b);
+      part[1][w][i] = part[1][w][i] * rescale2(a, m, cl2) +
+                      part[1][w + half][i] * rescale2(b, m, cl2);
+      part[2][w][i] += part[2][w + half][i];
+      part[0][w][i] = m;
+    }
+  }
+  if (w == 0 && t < T) {
+    const float top = part[0][0][i], rest = logf(part[1][0][i]);
+    lse[t] = r >= 0 ? fmaf(top, inv_tau, rest) : 0.f;
+    logp[t] = r >= 0 ? fmaf(part[2][0][i] - top, inv_tau, -rest) : 0.f;
+  }
 }
 
 // Hc row r = H row rowmap[r] for r < N; rows N .. (N rounded up to `round`)
@@ -780,7 +844,7 @@ cudaError_t launch_topk_merge(const float* unit_val, const int32_t* unit_id, con
 
 cudaError_t launch_mask_scan(const uint8_t* mask, int T, int* rowmap, int* invmap, int* n_count,
                              cudaStream_t stream) {
-  return launch_kernel("mask_scan", mask_scan_kernel, dim3(1), dim3(SCAN_THREADS), 0, stream, mask,
+  return launch_kernel("mask_scan", mask_scan_kernel<uint8_t>, dim3(1), dim3(SCAN_THREADS), 0, stream, mask,
                        T, rowmap, invmap, n_count);
 }
 
@@ -800,6 +864,31 @@ cudaError_t launch_f32_to_bf16(const float* in, uint16_t* out, long long n, int 
   return launch_kernel("f32_to_bf16", f32_to_bf16_kernel, dim3((unsigned)blocks), dim3(256), 0,
                        stream, reinterpret_cast<const float4*>(in), reinterpret_cast<uint2*>(out),
                        T, d / 4, invmap);
+}
+
+cudaError_t launch_grad_scan(const float* grad, int T, int* rowmap, int* invmap, int* n_count,
+                             cudaStream_t stream) {
+  return launch_kernel("grad_scan", mask_scan_kernel<float>, dim3(1), dim3(SCAN_THREADS), 0, stream,
+                       grad, T, rowmap, invmap, n_count);
+}
+
+cudaError_t launch_label_prep(const int32_t* ids, const int* rowmap, const int* n_count, int T,
+                              int V, int32_t* sidx, float* sp, int* status, cudaStream_t stream) {
+  return launch_kernel("label_prep", label_prep_kernel, dim3((T + 255) / 256), dim3(256), 0, stream,
+                       ids, rowmap, n_count, T, V, sidx, sp, status);
+}
+
+cudaError_t launch_logp_combine(const float* pm, const float* ps, const float* pd, int nsplit,
+                                int T, const int* invmap, float cl2, float inv_tau, float* logp,
+                                float* lse, cudaStream_t stream) {
+  // Few tokens: more threads on each one's splits, and more blocks.
+  if (T <= 4096)
+    return launch_kernel("logp_combine", logp_combine_kernel<4>, dim3((T + 3) / 4),
+                         dim3(COMBINE_THREADS), 0, stream, pm, ps, pd, nsplit, T, invmap, cl2,
+                         inv_tau, logp, lse);
+  return launch_kernel("logp_combine", logp_combine_kernel<32>, dim3((T + 31) / 32),
+                       dim3(COMBINE_THREADS), 0, stream, pm, ps, pd, nsplit, T, invmap, cl2,
+                       inv_tau, logp, lse);
 }
 
 }  // namespace kdkl

@@ -144,10 +144,12 @@ struct EpiParams {
   const uint8_t* mask;  // may be null (all tokens count)
   const int* n_count;   // number of counted tokens N
   float g_over_tau;
+  const float* row_grad;  // per caller token, or null: the row's scale is -row_grad * g_over_tau
   uint16_t* G;   // bf16 bits, [rows_pad, ldg]
   int64_t ldg;
   // EPI_STORE
   float* out;
+  uint16_t* out16;  // bf16 output instead of `out` (stored, not accumulated), or null
   int64_t ldo;
   int out_rows, out_cols;
   int accumulate;
@@ -768,6 +770,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
             const bool counted =
                 ep.rowmap || ep.mask == nullptr || __ldg(ep.mask + tok) != 0;
             scale = (counted && n > 0) ? ep.g_over_tau / (float)n : 0.f;
+            if (!MIX && ep.row_grad) scale = -__ldg(ep.row_grad + tok) * ep.g_over_tau;
             if (MIX) {
               lse12 = __ldg(ep.lse1 + tok) * 1.4426950408889634f;
               const float per_row = (counted && n > 0) ? 1.f / (float)n : 0.f;
@@ -942,7 +945,21 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
               }
             }
           } else {  // EPI_STORE
-            if (r < eo.out_rows) {
+            if (r < eo.out_rows && eo.out16) {
+              uint4* dst = reinterpret_cast<uint4*>(eo.out16 + (long long)r * eo.ldo + cl);
+              const int nvalid = min(32, eo.out_cols - cl);  // multiple of 8
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                if (8 * j < nvalid) {
+                  uint4 w;
+                  w.x = pack_bf16x2(v[8 * j + 0], v[8 * j + 1]);
+                  w.y = pack_bf16x2(v[8 * j + 2], v[8 * j + 3]);
+                  w.z = pack_bf16x2(v[8 * j + 4], v[8 * j + 5]);
+                  w.w = pack_bf16x2(v[8 * j + 6], v[8 * j + 7]);
+                  dst[j] = w;
+                }
+              }
+            } else if (r < eo.out_rows) {
               float* dst = eo.out + (long long)r * eo.ldo + cl;
               const int nvalid = min(32, eo.out_cols - cl);  // multiple of 4
 #pragma unroll

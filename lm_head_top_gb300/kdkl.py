@@ -49,6 +49,47 @@ class kd_topk_problem(ctypes.Structure):
 KDKL_TOPK_MAX_K = 512
 
 
+class kd_logprob_problem(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("d", ctypes.c_int64), ("V", ctypes.c_int64),
+                ("temperature", ctypes.c_float), ("dw_bf16", ctypes.c_int32),
+                ("chunk", ctypes.c_int64)]
+
+
+class kd_policy_problem(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("S", ctypes.c_int64), ("clip_low", ctypes.c_double),
+                ("clip_high", ctypes.c_double), ("dual_clip", ctypes.c_double),
+                ("kl_coef", ctypes.c_double), ("norm", ctypes.c_double),
+                ("reduction", ctypes.c_int32), ("advantage_per_sequence", ctypes.c_int32)]
+
+
+class kd_pref_problem(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("P", ctypes.c_int64), ("beta", ctypes.c_double),
+                ("label_smoothing", ctypes.c_double), ("margin", ctypes.c_double),
+                ("kind", ctypes.c_int32), ("average", ctypes.c_int32), ("halves", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class kd_adamw_tensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p),
+                ("exp_avg", ctypes.c_void_p), ("exp_avg_sq", ctypes.c_void_p),
+                ("copy", ctypes.c_void_p), ("m_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n", ctypes.c_int64), ("decay", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class kd_adamw_options(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double),
+                ("step", ctypes.c_int64), ("grad_scale_dev", ctypes.c_void_p),
+                ("grad_scale", ctypes.c_float), ("param_bf16", ctypes.c_int32),
+                ("grad_bf16", ctypes.c_int32), ("state_8bit", ctypes.c_int32)]
+
+
+KD_REDUCTIONS = {"token": 0, "sequence": 1, "sum": 2}
+KD_PREF_KINDS = {"sigmoid": 0, "ipo": 1, "hinge": 2}
+KD_ADAMW_BLOCK = 256  # elements that share one scale of an 8-bit state
+
+
 class kd_kernel_time(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 32), ("launches", ctypes.c_int64),
                 ("total_ms", ctypes.c_double)]
@@ -86,6 +127,20 @@ _SIGS = {
     "kd_lmhead_topk_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(kd_topk_problem)]),
     "kd_lmhead_topk": (ctypes.c_int, [ctypes.POINTER(kd_topk_problem), _P, _P, _P, _P, _P,
                                       ctypes.c_size_t, _P]),
+    "kd_logprob_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(kd_logprob_problem),
+                                                    ctypes.c_int]),
+    "kd_logprob_forward": (ctypes.c_int, [ctypes.POINTER(kd_logprob_problem), _P, _P, _P, _P, _P,
+                                          _P, _P, ctypes.c_size_t, _P]),
+    "kd_logprob_backward": (ctypes.c_int, [ctypes.POINTER(kd_logprob_problem), _P, _P, _P, _P, _P,
+                                           _P, _P, ctypes.c_int, _P, ctypes.c_size_t, _P]),
+    "kd_policy_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(kd_policy_problem)]),
+    "kd_policy_loss": (ctypes.c_int, [ctypes.POINTER(kd_policy_problem), _P, _P, _P, _P, _P, _P,
+                                      ctypes.c_float, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "kd_pref_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(kd_pref_problem)]),
+    "kd_pref_loss": (ctypes.c_int, [ctypes.POINTER(kd_pref_problem), _P, _P, _P, _P,
+                                    ctypes.c_float, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "kd_adamw_step": (ctypes.c_int, [ctypes.POINTER(kd_adamw_tensor), ctypes.c_int32,
+                                     ctypes.POINTER(kd_adamw_options), _P]),
     "kd_kl_check_status": (ctypes.c_int, [_P, _P]),
     "kd_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "kd_launch_count": (ctypes.c_int64, []),
@@ -444,6 +499,269 @@ def kd_lmhead_topk(H, W, K, *, topk_idx=None, topk_logit=None, workspace=None, s
     _call("kd_lmhead_topk", dev, stream, ctypes.byref(p), _ptr(H), _ptr(W), _ptr(topk_idx),
           _ptr(topk_logit), _ptr(workspace), workspace.numel())
     return topk_idx, topk_logit
+
+
+def _new(shape, dtype, dev, stream):
+    """An output or workspace made here for a call on ``stream``: allocated as
+    that stream's own memory, so that it is not handed to another stream's
+    tensors while the call still runs."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _given_workspace(workspace, need, where, dev, stream):
+    if need == 0:
+        raise KDKLError(2, where)
+    if workspace is None:
+        return _new(need, torch.uint8, dev, stream)
+    _check(workspace, "workspace", torch.uint8, (workspace.numel(),))
+    same_device(dev, workspace=workspace)
+    return workspace
+
+
+def kd_logprob_workspace_size(T, d, V, temperature=1.0, chunk=1024, which=0,
+                              dW_dtype=torch.float32) -> int:
+    p = kd_logprob_problem(int(T), int(d), int(V), float(temperature),
+                           1 if dW_dtype == torch.bfloat16 else 0, int(chunk))
+    return int(load().kd_logprob_workspace_size(ctypes.byref(p), int(which)))
+
+
+def _logprob_args(H, W, ids):
+    T, d = H.shape
+    V = W.shape[0]
+    _check(H, "H", torch.bfloat16, (T, d))
+    _check(W, "W", torch.bfloat16, (V, d))
+    _check(ids, "ids", torch.int32, (T,))
+    same_device(H.device, W=W, ids=ids)
+    return T, d, V, H.device
+
+
+def kd_logprob_forward(H, W, ids, mask=None, *, temperature=1.0, logp=None, lse=None,
+                       workspace=None, stream=None):
+    """Log-probability of ids[t] under softmax(H[t] . W^T / temperature), the logits
+    never stored. Returns (logp [T] fp32, lse [T] fp32); masked tokens read 0."""
+    T, d, V, dev = _logprob_args(H, W, ids)
+    if mask is not None:
+        _check(mask, "mask", torch.uint8, (T,))
+        same_device(dev, mask=mask)
+    p = kd_logprob_problem(T, d, V, float(temperature), 0, 1)
+    workspace = _given_workspace(workspace, load().kd_logprob_workspace_size(ctypes.byref(p), 0),
+                                 "kd_logprob_workspace_size", dev, stream)
+    logp = _out(logp, "logp", torch.float32, (T,), dev)
+    lse = _out(lse, "lse", torch.float32, (T,), dev)
+    logp = _new(T, torch.float32, dev, stream) if logp is None else logp
+    lse = _new(T, torch.float32, dev, stream) if lse is None else lse
+    _call("kd_logprob_forward", dev, stream, ctypes.byref(p), _ptr(H), _ptr(W), _ptr(ids),
+          _ptr(mask), _ptr(logp), _ptr(lse), _ptr(workspace), workspace.numel())
+    return logp, lse
+
+
+def kd_logprob_backward(H, W, ids, lse, grad_logp, *, temperature=1.0, chunk=1024, dH=None,
+                        dW=None, dW_dtype=torch.float32, accumulate_dW=False, workspace=None,
+                        stream=None):
+    """Gradients of sum_t grad_logp[t] * logp[t]. Returns (dH [T,d] bf16, dW [V,d] in
+    ``dW_dtype``: fp32, which may be added to, or bf16). Tokens whose gradient is
+    zero are skipped."""
+    T, d, V, dev = _logprob_args(H, W, ids)
+    _check(lse, "lse", torch.float32, (T,))
+    _check(grad_logp, "grad_logp", torch.float32, (T,))
+    same_device(dev, lse=lse, grad_logp=grad_logp)
+    if dW is not None:
+        dW_dtype = dW.dtype
+    if dW_dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("dW must be torch.float32 or torch.bfloat16, got %s" % dW_dtype)
+    dH = _out(dH, "dH", torch.bfloat16, (T, d), dev)
+    dW = _out(dW, "dW", dW_dtype, (V, d), dev)
+    if accumulate_dW and dW is None:
+        raise ValueError("accumulate_dW needs an existing dW")
+    if accumulate_dW and dW_dtype == torch.bfloat16:
+        raise ValueError("a bf16 dW is not accumulated: pass an fp32 one")
+    p = kd_logprob_problem(T, d, V, float(temperature), 1 if dW_dtype == torch.bfloat16 else 0,
+                           int(chunk))
+    workspace = _given_workspace(workspace, load().kd_logprob_workspace_size(ctypes.byref(p), 1),
+                                 "kd_logprob_workspace_size", dev, stream)
+    dH = _new((T, d), torch.bfloat16, dev, stream) if dH is None else dH
+    dW = _new((V, d), dW_dtype, dev, stream) if dW is None else dW
+    _call("kd_logprob_backward", dev, stream, ctypes.byref(p), _ptr(H), _ptr(W), _ptr(ids),
+          _ptr(lse), _ptr(grad_logp), _ptr(dH), _ptr(dW), 1 if accumulate_dW else 0,
+          _ptr(workspace), workspace.numel())
+    return dH, dW
+
+
+def kd_policy_loss(logp, old_logp, ref_logp, advantages, mask=None, cu_seqlens=None, *,
+                   clip_low=0.2, clip_high=0.2, dual_clip=0.0, kl_coef=0.0, reduction="token",
+                   norm=1.0, grad_loss=1.0, want_grad=True, loss=None, stats=None, grad_logp=None,
+                   workspace=None, stream=None):
+    """Clipped policy loss with a KL term over packed sequences, and its gradient.
+
+    logp, old_logp (None: ratio 1), ref_logp (None: no KL term): [T] fp32.
+    advantages: [T], or one per sequence of ``cu_seqlens`` ([S+1] int32).
+    reduction: "token" (mean over counted tokens), "sequence" (mean over the
+    sequences of each one's mean) or "sum" (sum / ``norm``).
+    Returns (loss [1], stats [3] = policy part, KL part, share of clipped tokens,
+    grad_logp [T] = grad_loss * dloss/dlogp or None)."""
+    T = logp.numel()
+    dev = logp.device
+    _check(logp, "logp", torch.float32, (T,))
+    for name, t in (("old_logp", old_logp), ("ref_logp", ref_logp)):
+        if t is not None:
+            _check(t, name, torch.float32, (T,))
+    if mask is not None:
+        _check(mask, "mask", torch.uint8, (T,))
+    S = 0
+    if cu_seqlens is not None:
+        S = max(0, cu_seqlens.numel() - 1)
+        _check(cu_seqlens, "cu_seqlens", torch.int32, (S + 1,))
+    per_sequence = cu_seqlens is not None and advantages.numel() == S and S != T
+    _check(advantages, "advantages", torch.float32, (S if per_sequence else T,))
+    same_device(dev, old_logp=old_logp, ref_logp=ref_logp, advantages=advantages, mask=mask,
+                cu_seqlens=cu_seqlens)
+    if reduction not in KD_REDUCTIONS:
+        raise ValueError("reduction must be one of %s, got %r" % (sorted(KD_REDUCTIONS), reduction))
+    p = kd_policy_problem(T, S, clip_low, clip_high, dual_clip, kl_coef if ref_logp is not None
+                          else 0.0, norm, KD_REDUCTIONS[reduction], 1 if per_sequence else 0)
+    need = load().kd_policy_workspace_size(ctypes.byref(p))
+    workspace = _given_workspace(workspace, need, "kd_policy_workspace_size", dev, stream) \
+        if need else _new(256, torch.uint8, dev, stream)  # the call names the error
+    loss = _out(loss, "loss", torch.float32, (1,), dev)
+    stats = _out(stats, "stats", torch.float32, (3,), dev)
+    grad_logp = _out(grad_logp, "grad_logp", torch.float32, (T,), dev)
+    loss = _new(1, torch.float32, dev, stream) if loss is None else loss
+    stats = _new(3, torch.float32, dev, stream) if stats is None else stats
+    if want_grad and grad_logp is None:
+        grad_logp = _new(T, torch.float32, dev, stream)
+    _call("kd_policy_loss", dev, stream, ctypes.byref(p), _ptr(logp), _ptr(old_logp),
+          _ptr(ref_logp), _ptr(advantages), _ptr(mask), _ptr(cu_seqlens), float(grad_loss),
+          _ptr(loss), _ptr(stats), _ptr(grad_logp), _ptr(workspace), workspace.numel())
+    return loss, stats, grad_logp
+
+
+def kd_pref_loss(logp, ref_logp, cu_seqlens, mask=None, *, beta=0.1, kind="sigmoid",
+                 label_smoothing=0.0, margin=0.0, average=False, halves=False, grad_loss=1.0,
+                 want_grad=True, loss=None, rewards=None, grad_logp=None, workspace=None,
+                 stream=None):
+    """Preference loss over pairs (chosen, rejected) of packed sequences, and its gradient.
+
+    logp, ref_logp (None: no reference): [T] fp32; cu_seqlens: [2P+1] int32, sequences
+    2i and 2i+1 forming pair i, or with ``halves`` i and P + i. ``average``: a
+    sequence counts with the mean of its tokens' log ratios instead of their sum.
+    Returns (loss [1], rewards [P,2], grad_logp [T] = grad_loss * dloss/dlogp or None)."""
+    T = logp.numel()
+    dev = logp.device
+    _check(logp, "logp", torch.float32, (T,))
+    if ref_logp is not None:
+        _check(ref_logp, "ref_logp", torch.float32, (T,))
+    if mask is not None:
+        _check(mask, "mask", torch.uint8, (T,))
+    n = cu_seqlens.numel()
+    _check(cu_seqlens, "cu_seqlens", torch.int32, (n,))
+    if n % 2 != 1:
+        raise ValueError("cu_seqlens holds 2 P + 1 offsets, got %d" % n)
+    P = n // 2
+    same_device(dev, ref_logp=ref_logp, mask=mask, cu_seqlens=cu_seqlens)
+    if kind not in KD_PREF_KINDS:
+        raise ValueError("kind must be one of %s, got %r" % (sorted(KD_PREF_KINDS), kind))
+    p = kd_pref_problem(T, P, beta, label_smoothing, margin, KD_PREF_KINDS[kind],
+                        1 if average else 0, 1 if halves else 0, 0)
+    need = load().kd_pref_workspace_size(ctypes.byref(p))
+    workspace = _given_workspace(workspace, need, "kd_pref_workspace_size", dev, stream) \
+        if need else _new(256, torch.uint8, dev, stream)  # the call names the error
+    loss = _out(loss, "loss", torch.float32, (1,), dev)
+    rewards = _out(rewards, "rewards", torch.float32, (P, 2), dev)
+    grad_logp = _out(grad_logp, "grad_logp", torch.float32, (T,), dev)
+    loss = _new(1, torch.float32, dev, stream) if loss is None else loss
+    rewards = _new((P, 2), torch.float32, dev, stream) if rewards is None else rewards
+    if want_grad and grad_logp is None:
+        grad_logp = _new(T, torch.float32, dev, stream)
+    _call("kd_pref_loss", dev, stream, ctypes.byref(p), _ptr(logp), _ptr(ref_logp), _ptr(mask),
+          _ptr(cu_seqlens), float(grad_loss), _ptr(loss), _ptr(rewards), _ptr(grad_logp),
+          _ptr(workspace), workspace.numel())
+    return loss, rewards, grad_logp
+
+
+class KDAdamWTensors:
+    """The tensors of an AdamW step, checked once: the host table that kd_adamw_step
+    passes to the library, and the tensors it points to (kept alive, not copied)."""
+
+    def __init__(self, table, n, device, tensors, param_bf16, grad_bf16, state_8bit):
+        self.table, self.n, self.device, self.tensors = table, n, device, tensors
+        self.param_bf16, self.grad_bf16, self.state_8bit = param_bf16, grad_bf16, state_8bit
+
+
+def kd_adamw_tensors(params, grads, exp_avg, exp_avg_sq, *, copies=None, m_scales=None,
+                     v_scales=None, decay=None) -> KDAdamWTensors:
+    """The list of tensors for kd_adamw_step; make it again when a tensor is replaced.
+
+    params: fp32 or bf16; grads: fp32 or bf16. exp_avg / exp_avg_sq: fp32 (m and v), or
+    torch.float8_e4m3fn (m and sqrt(v)) with ``m_scales`` / ``v_scales``: fp32, one for
+    every 256 elements of a tensor (start from zeros, and ones for the scales).
+    copies: bf16 tensors that receive the new parameters. decay: per tensor, whether
+    weight decay applies (default: to all)."""
+    n = len(params)
+    lists = {"params": params, "grads": grads, "exp_avg": exp_avg, "exp_avg_sq": exp_avg_sq,
+             "copies": copies, "m_scales": m_scales, "v_scales": v_scales}
+    for name, ts in lists.items():
+        if ts is not None and len(ts) != n:
+            raise ValueError("%s has %d tensors, expected %d" % (name, len(ts), n))
+    if decay is not None and len(decay) != n:
+        raise ValueError("decay has %d values, expected %d" % (len(decay), n))
+    if n == 0:
+        return KDAdamWTensors((kd_adamw_tensor * 1)(), 0, None, lists, 0, 0, 0)
+    dev = params[0].device
+    p_t, g_t, s_t = params[0].dtype, grads[0].dtype, exp_avg[0].dtype
+    if p_t not in (torch.float32, torch.bfloat16):
+        raise TypeError("params must be torch.float32 or torch.bfloat16, got %s" % p_t)
+    if g_t not in (torch.float32, torch.bfloat16):
+        raise TypeError("grads must be torch.float32 or torch.bfloat16, got %s" % g_t)
+    if s_t not in (torch.float32, torch.float8_e4m3fn):
+        raise TypeError("states must be torch.float32 or torch.float8_e4m3fn, got %s" % s_t)
+    s8 = s_t == torch.float8_e4m3fn
+    if s8 and (m_scales is None or v_scales is None):
+        raise ValueError("8-bit states need m_scales and v_scales")
+    table = (kd_adamw_tensor * n)()
+    for i in range(n):
+        shape, count = tuple(params[i].shape), params[i].numel()
+        blocks = (count + KD_ADAMW_BLOCK - 1) // KD_ADAMW_BLOCK
+        _check(params[i], "params[%d]" % i, p_t, shape)
+        _check(grads[i], "grads[%d]" % i, g_t, shape)
+        _check(exp_avg[i], "exp_avg[%d]" % i, s_t, shape)
+        _check(exp_avg_sq[i], "exp_avg_sq[%d]" % i, s_t, shape)
+        if copies is not None:
+            _check(copies[i], "copies[%d]" % i, torch.bfloat16, shape)
+        if s8:
+            _check(m_scales[i], "m_scales[%d]" % i, torch.float32, (blocks,))
+            _check(v_scales[i], "v_scales[%d]" % i, torch.float32, (blocks,))
+        row = table[i]
+        for field, ts in (("param", params), ("grad", grads), ("exp_avg", exp_avg),
+                          ("exp_avg_sq", exp_avg_sq), ("copy", copies),
+                          ("m_scale", m_scales if s8 else None),
+                          ("v_scale", v_scales if s8 else None)):
+            if ts is not None:
+                if ts[i].device != dev:
+                    raise ValueError("%s of tensor %d is on %s, expected %s"
+                                     % (field, i, ts[i].device, dev))
+                setattr(row, field, ts[i].data_ptr())
+        row.n = count
+        row.decay = 1 if decay is None or decay[i] else 0
+    return KDAdamWTensors(table, n, dev, lists, 1 if p_t == torch.bfloat16 else 0,
+                          1 if g_t == torch.bfloat16 else 0, 1 if s8 else 0)
+
+
+def kd_adamw_step(tensors: KDAdamWTensors, *, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0,
+                  step=1, grad_scale=1.0, grad_scale_dev=None, stream=None) -> None:
+    """One AdamW step, in place, on the tensors of kd_adamw_tensors. ``step`` counts from 1.
+    The gradients are multiplied by ``grad_scale`` and, if given, by the device scalar
+    ``grad_scale_dev`` ([1] fp32, a clip coefficient)."""
+    if grad_scale_dev is not None:
+        _check(grad_scale_dev, "grad_scale_dev", torch.float32, (1,))
+        same_device(tensors.device, grad_scale_dev=grad_scale_dev)
+    o = kd_adamw_options(lr, betas[0], betas[1], eps, weight_decay, int(step),
+                         None if grad_scale_dev is None else grad_scale_dev.data_ptr(), grad_scale,
+                         tensors.param_bf16, tensors.grad_bf16, tensors.state_8bit)
+    if tensors.n:
+        _call("kd_adamw_step", tensors.device, stream, tensors.table, tensors.n, ctypes.byref(o))
 
 
 def kd_kl_check_status(workspace: torch.Tensor, stream=None) -> int:
