@@ -53,6 +53,31 @@ cudaError_t launch_kernel_cluster(const char* name, void (*kern)(KArgs...), dim3
   return e;
 }
 
+// Same, allowed to start before the launch ahead of it in the stream has ended:
+// the kernel waits for it (griddepcontrol.wait) before it reads what that one
+// writes or writes what it reads. For kernels of a few microseconds, whose
+// launch and first lookups are a large share. (An event between
+// two launches orders them fully.)
+template <typename... KArgs, typename... Args>
+cudaError_t launch_kernel_early(const char* name, void (*kern)(KArgs...), dim3 grid, dim3 block,
+                                cudaStream_t stream, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  void* token = nullptr;
+  note_launch_begin(name, stream, &token);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  note_launch_end(token, stream);
+  return e;
+}
+
 // kernels_small.cu
 // rowmap == nullptr: row t <- token t, and the mask is counted into *n_count.
 // Else row r <- token rowmap[r] for r < *n_count (set by launch_mask_scan).
@@ -165,10 +190,10 @@ struct PolicyArgs {
   float inv_norm, kl_coef, grad_loss;
   float r_low, r_high, r_dual;                                       // clipped ratios
   float low_hi, low_lo, high_hi, high_lo, dual_hi, dual_lo;          // borders of logp - old_logp
-  int* n_count;        // [0] counted tokens, [1] sequences that have any
+  int* n_count;        // [0] counted tokens, [1] sequences that have any, [2] clipped tokens
   int* n_seq;          // [S] counted tokens of each sequence
-  int* ticket;         // [2] blocks done (loss, count)
-  double* block_part;  // [blocks, 3]
+  int* ticket;         // blocks done
+  float4* block_part;  // [blocks] the two sums, each in two floats
   float *loss, *stats, *grad;
 };
 struct PrefArgs {
@@ -176,19 +201,22 @@ struct PrefArgs {
   const uint8_t* mask;
   const int32_t* cu;
   int T, P, vec, kind, average, halves;
-  double beta, label_smoothing, margin, grad_loss;
-  double* slot_sum;   // [blocks + 2P]
-  int* slot_n;        // [blocks + 2P]
-  double* pair_loss;  // [P]
+  float beta, half_inv_beta, label_smoothing, margin, grad_over_P;
+  float2* slot_sum;   // [warps + 2P] in two floats
+  int* slot_n;        // [warps + 2P]
+  float* pair_loss;   // [P]
   float* coef;        // [2P] gradient of a sequence's counted tokens
-  int* ticket;
   float *loss, *rewards, *grad;
 };
 // Masks of up to so many tokens are counted by every block of the loss kernel for itself.
 constexpr int kPolicyCountHere = 32768;
-int seq_blocks(int T);
-cudaError_t launch_policy_loss(const PolicyArgs& a, int* status, cudaStream_t stream);
-cudaError_t launch_pref_loss(const PrefArgs& a, int* status, cudaStream_t stream);
+// Batches that one block takes: one launch, and no memory to clear before it.
+inline bool policy_one_block(int T, int reduction) { return T <= 4096 && reduction != 1; }
+inline bool pref_one_block(int T, int P) { return T <= 8192 && P <= 256; }
+int seq_blocks(int T, int num_sms);
+int seq_warps(int T, int num_sms);
+cudaError_t launch_policy_loss(const PolicyArgs& a, int num_sms, int* status, cudaStream_t stream);
+cudaError_t launch_pref_loss(const PrefArgs& a, int num_sms, int* status, cudaStream_t stream);
 
 // kernels_adamw.cu
 struct AdamTensor {

@@ -11,7 +11,9 @@
 namespace kdkl {
 namespace {
 
-constexpr size_t kHeader = 256;  // int status; counted tokens; sequences with any; two tickets
+constexpr size_t kHeader = 256;  // int status; three counts; a ticket
+// Bound on the SM count that sizes workspaces (the same with and without a device).
+constexpr int kMaxSms = 256;
 constexpr int64_t kMaxTokens = (1ll << 31) - 4096;  // a block's token indexes stay in 31 bits
 
 inline size_t pad256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -22,11 +24,11 @@ T* place(void* ws, size_t off) {
   return reinterpret_cast<T*>(static_cast<char*>(ws) + off);
 }
 
-// Vector accesses of eight tokens at a time.
+// Vector accesses: 16 bytes of every array.
 bool vectors(const void* a, const void* b, const void* c, const void* d, const void* e,
              const uint8_t* mask) {
   return aligned_to(a, 16) && aligned_to(b, 16) && aligned_to(c, 16) && aligned_to(d, 16) &&
-         aligned_to(e, 16) && aligned_to(mask, 8);
+         aligned_to(e, 16) && aligned_to(mask, 16);
 }
 
 // A border in 48 bits: the nearest float and the remainder.
@@ -42,7 +44,7 @@ PolicyLayout policy_layout(const kd_policy_problem& p) {
   PolicyLayout L{};
   L.off_seq = kHeader;
   L.off_part = pad256(L.off_seq + (size_t)p.S * 4);
-  L.total = pad256(L.off_part + (size_t)seq_blocks((int)p.T) * 3 * 8);
+  L.total = pad256(L.off_part + (size_t)seq_blocks((int)p.T, kMaxSms) * 16);
   return L;
 }
 
@@ -67,11 +69,11 @@ struct PrefLayout {
 };
 PrefLayout pref_layout(const kd_pref_problem& p) {
   PrefLayout L{};
-  const size_t slots = (size_t)seq_blocks((int)p.T) + 2 * (size_t)p.P;
+  const size_t slots = std::max<size_t>(seq_warps((int)p.T, kMaxSms), 64) + 2 * (size_t)p.P;
   L.off_sum = kHeader;
   L.off_n = pad256(L.off_sum + slots * 8);
   L.off_pair = pad256(L.off_n + slots * 4);
-  L.off_coef = pad256(L.off_pair + (size_t)p.P * 8);
+  L.off_coef = pad256(L.off_pair + (size_t)p.P * 4);
   L.total = pad256(L.off_coef + 2 * (size_t)p.P * 4);
   return L;
 }
@@ -120,9 +122,12 @@ kd_status kd_policy_loss(const kd_policy_problem* prob, const float* logp, const
   int sms = 0;
   if ((st = (kd_status)current_device(&sms)) != KD_OK) return st;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
-  // status, counts, tickets and the sequences' counts start at zero
+  sms = std::min(sms, kMaxSms);
+  // status, counts, ticket and the sequences' counts start at zero
   const size_t zeros = p.reduction == KD_REDUCE_SEQUENCE ? L.off_part : kHeader;
-  if (cudaMemsetAsync(workspace, 0, zeros, stream) != cudaSuccess) return KD_ERR_CUDA;
+  if ((p.T == 0 || !policy_one_block((int)p.T, p.reduction)) &&
+      cudaMemsetAsync(workspace, 0, zeros, stream) != cudaSuccess)
+    return KD_ERR_CUDA;
   if (p.T == 0) {
     if (cudaMemsetAsync(loss, 0, 4, stream) != cudaSuccess) return KD_ERR_CUDA;
     if (stats && cudaMemsetAsync(stats, 0, 12, stream) != cudaSuccess) return KD_ERR_CUDA;
@@ -155,12 +160,12 @@ kd_status kd_policy_loss(const kd_policy_problem* prob, const float* logp, const
   if (a.dual) split_border(log(p.dual_clip), &a.dual_hi, &a.dual_lo);
   a.n_count = status + 1;
   a.n_seq = place<int>(workspace, L.off_seq);
-  a.ticket = status + 3;
-  a.block_part = place<double>(workspace, L.off_part);
+  a.ticket = status + 4;
+  a.block_part = place<float4>(workspace, L.off_part);
   a.loss = loss;
   a.stats = stats;
   a.grad = grad_logp;
-  return launch_policy_loss(a, status, stream) == cudaSuccess ? KD_OK : KD_ERR_CUDA;
+  return launch_policy_loss(a, sms, status, stream) == cudaSuccess ? KD_OK : KD_ERR_CUDA;
 }
 
 size_t kd_pref_workspace_size(const kd_pref_problem* prob) {
@@ -187,8 +192,11 @@ kd_status kd_pref_loss(const kd_pref_problem* prob, const float* logp, const flo
   int sms = 0;
   if ((st = (kd_status)current_device(&sms)) != KD_OK) return st;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
-  if (cudaMemsetAsync(workspace, 0, kHeader, stream) != cudaSuccess) return KD_ERR_CUDA;
-  if (p.P == 0) return cudaMemsetAsync(loss, 0, 4, stream) == cudaSuccess ? KD_OK : KD_ERR_CUDA;
+  sms = std::min(sms, kMaxSms);
+  if (p.P == 0) {
+    if (cudaMemsetAsync(workspace, 0, kHeader, stream) != cudaSuccess) return KD_ERR_CUDA;
+    return cudaMemsetAsync(loss, 0, 4, stream) == cudaSuccess ? KD_OK : KD_ERR_CUDA;
+  }
   int* status = place<int>(workspace, 0);
   PrefArgs a{};
   a.logp = logp;
@@ -201,19 +209,19 @@ kd_status kd_pref_loss(const kd_pref_problem* prob, const float* logp, const flo
   a.kind = p.kind;
   a.average = p.average;
   a.halves = p.halves;
-  a.beta = p.beta;
-  a.label_smoothing = p.label_smoothing;
-  a.margin = p.margin;
-  a.grad_loss = (double)grad_loss;
-  a.slot_sum = place<double>(workspace, L.off_sum);
+  a.beta = (float)p.beta;
+  a.label_smoothing = (float)p.label_smoothing;
+  a.margin = (float)p.margin;
+  a.half_inv_beta = (float)(0.5 / p.beta);
+  a.grad_over_P = (float)((double)grad_loss / (double)p.P);
+  a.slot_sum = place<float2>(workspace, L.off_sum);
   a.slot_n = place<int>(workspace, L.off_n);
-  a.pair_loss = place<double>(workspace, L.off_pair);
+  a.pair_loss = place<float>(workspace, L.off_pair);
   a.coef = place<float>(workspace, L.off_coef);
-  a.ticket = status + 3;
   a.loss = loss;
   a.rewards = rewards;
   a.grad = grad_logp;
-  return launch_pref_loss(a, status, stream) == cudaSuccess ? KD_OK : KD_ERR_CUDA;
+  return launch_pref_loss(a, sms, status, stream) == cudaSuccess ? KD_OK : KD_ERR_CUDA;
 }
 
 kd_status kd_adamw_step(const kd_adamw_tensor* tensors, int32_t n_tensors,

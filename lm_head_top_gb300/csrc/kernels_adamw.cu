@@ -3,9 +3,10 @@
 //   g' = g * grad_scale            m' = b1 m + (1 - b1) g'
 //   v' = b2 v + (1 - b2) g'^2      p' = p (1 - lr wd) - lr/(1-b1^t) * m' / (sqrt(v') / sqrt(1-b2^t) + eps)
 //
-// Every product, sum, root and quotient is rounded to fp32 by itself, in the
-// order written (no contraction into fused multiply-adds): the results are
-// those of the elementwise formula, bit for bit, whichever path computes them.
+// Every product and sum is rounded to fp32 by itself, in the order written (no
+// contraction into fused multiply-adds), so m' and v' are those of the
+// elementwise formula, bit for bit, whichever path computes them; with 32-bit
+// states so are the root and the quotient, and p'.
 //
 // 8-bit states: m and the root r = sqrt(v) are held in e4m3, 256 consecutive
 // elements sharing one fp32 power of two, the least with which the block's
@@ -15,7 +16,11 @@
 // alone). This step's update uses the 32-bit m' and sqrt(v'); only what is
 // kept for the next step is rounded to 8 bits (m to a relative 2^-4, the root
 // likewise: what the user chose when asking for 8-bit states). A power of two
-// as the scale makes scaling exact, so e4m3 is the only rounding.
+// as the scale makes scaling exact, so e4m3 is the only rounding. With 16 to 22
+// bytes an element the correctly rounded root and quotient are what the kernel
+// would wait for (64 % of issue slots at 69 % of the DRAM rate), so here they
+// are the hardware's approximations: 2 ulp of the step, which is a thousandth
+// of p, and of a root that is about to lose 20 bits.
 //
 // What bounds it: DRAM. Read g, p, m, v and write p, m, v (and the bf16 copy):
 // 30 bytes per element with fp32 gradients, 32-bit states and a copy.
@@ -159,19 +164,12 @@ __device__ __forceinline__ void store_e4m3(uint8_t* p, long long i, long long n,
   }
 }
 
-// The scale block's largest finite magnitude over the warp, then the least
-// power of two (not below 2^-126) that keeps it within 512 * 0.904383 = 463.04,
-// which rounds to 448. (448 itself, or any border of few bits, is met exactly by
-// sums of 8-bit states and bf16 gradients, and the last bit of such a sum would
-// then set the scale.) An all-zero block gets 1.
-__device__ __forceinline__ float block_scale(const Vec8& r) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int j = 0; j < ADAM_VEC; ++j) {
-    const uint32_t a = __float_as_uint(r.x[j]) & 0x7fffffffu;
-    top = max(top, a < 0x7f800000u ? a : 0u);  // infinities and NaN do not set the scale
-  }
-  top = __reduce_max_sync(0xffffffffu, top);
+// Least power of two (not below 2^-126) that keeps a block whose largest
+// magnitude is `top` (finite, as bits) within 512 * 0.904383 = 463.04, which
+// rounds to 448. (448 itself, or any border of few bits, is met exactly by sums
+// of 8-bit states and bf16 gradients, and the last bit of such a sum would then
+// set the scale.) An all-zero block gets 1.
+__device__ __forceinline__ float scale_for(uint32_t top) {
   if (top == 0u) return 1.f;
   const float half = __uint_as_float((top & 0x7fffffu) | 0x3f000000u);  // in [0.5, 1)
   const int e = (int)(top >> 23) - 126 - 9 + (half > 0.904383f ? 1 : 0);
@@ -182,17 +180,29 @@ __device__ __forceinline__ float pow2_inverse(float s) {  // s = 2^e, -126 <= e 
   return __uint_as_float(0x7f000000u - __float_as_uint(s));
 }
 
-// Finite values in units of the block's scale; infinities become NaN, which
-// e4m3 can hold and infinities it cannot.
-__device__ __forceinline__ Vec8 in_units(const Vec8& r, float scale) {
-  const float inv = pow2_inverse(scale);
-  Vec8 q;
+constexpr uint32_t kInfBits = 0x7f800000u;
+
+// Bits of the warp's largest magnitude; NaN are passed over.
+__device__ __forceinline__ uint32_t warp_top(const Vec8& r) {
+  float a = 0.f;
 #pragma unroll
-  for (int j = 0; j < ADAM_VEC; ++j) {
-    const float y = __fmul_rn(r.x[j], inv);
-    q.x[j] = fabsf(r.x[j]) < INFINITY ? y : __uint_as_float(0x7fffffffu);
-  }
-  return q;
+  for (int j = 0; j < ADAM_VEC; ++j) a = fmaxf(a, fabsf(r.x[j]));
+  return __reduce_max_sync(0xffffffffu, __float_as_uint(a));
+}
+
+// A block that holds infinities: they set no scale and are kept as NaN, which
+// e4m3 has and infinities it has not.
+__device__ __forceinline__ uint32_t drop_infinities(Vec8& r) {
+#pragma unroll
+  for (int j = 0; j < ADAM_VEC; ++j)
+    if (fabsf(r.x[j]) == INFINITY) r.x[j] = __uint_as_float(0x7fffffffu);
+  return warp_top(r);
+}
+
+__device__ __forceinline__ float sqrt_approx(float x) {
+  float y;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 template <typename P, typename G, bool STATE8, int CAP>
@@ -240,24 +250,34 @@ __global__ void __launch_bounds__(ADAM_THREADS)
       const float gj = __fmul_rn(g.x[j], gs);
       m.x[j] = __fadd_rn(__fmul_rn(m.x[j], s.b1), __fmul_rn(gj, s.one_b1));
       v.x[j] = __fadd_rn(__fmul_rn(v.x[j], s.b2), __fmul_rn(__fmul_rn(gj, gj), s.one_b2));
-      root.x[j] = __fsqrt_rn(v.x[j]);
+      root.x[j] = STATE8 ? sqrt_approx(v.x[j]) : __fsqrt_rn(v.x[j]);
       const float den = __fadd_rn(__fmul_rn(root.x[j], s.inv_root_bc2), s.eps);
-      const float u = __fmul_rn(__fdiv_rn(m.x[j], den), s.step);
+      const float q = STATE8 ? __fdividef(m.x[j], den) : __fdiv_rn(m.x[j], den);
+      const float u = __fmul_rn(q, s.step);
       p.x[j] = __fsub_rn(__fmul_rn(p.x[j], keep), u);
     }
     store8(static_cast<P*>(t.param), i, n, vec, p);
     if (t.copy) store8(t.copy, i, n, vec, p);
     if (STATE8) {
-      // Elements past n are zero here and set no scale.
-      const float ms = block_scale(m), vs = block_scale(root);
-      const Vec8 qm = in_units(m, ms);
-      Vec8 qr = in_units(root, vs);
+      // Elements past n are zero here and set no scale. The root's scale comes
+      // from the largest v by one correctly rounded root.
+      uint32_t top_m = warp_top(m), top_v = warp_top(v);
+      if (top_m == kInfBits) top_m = drop_infinities(m);
+      if (top_v == kInfBits) {
+        drop_infinities(root);
+        top_v = drop_infinities(v);
+      }
+      const float ms = scale_for(top_m);
+      const float vs = scale_for(__float_as_uint(__fsqrt_rn(__uint_as_float(top_v))));
+      const float inv_m = pow2_inverse(ms), inv_v = pow2_inverse(vs);
 #pragma unroll
-      for (int j = 0; j < ADAM_VEC; ++j)
-        if (root.x[j] > 0.f && root.x[j] < INFINITY)
-          qr.x[j] = fmaxf(qr.x[j], 0.001953125f);  // 2^-9, e4m3's least step
-      store_e4m3(static_cast<uint8_t*>(t.exp_avg), i, n, vec, qm);
-      store_e4m3(static_cast<uint8_t*>(t.exp_avg_sq), i, n, vec, qr);
+      for (int j = 0; j < ADAM_VEC; ++j) {
+        m.x[j] *= inv_m;
+        const float y = root.x[j] * inv_v;
+        root.x[j] = root.x[j] > 0.f ? fmaxf(y, 0.001953125f) : y;  // 2^-9, e4m3's least step
+      }
+      store_e4m3(static_cast<uint8_t*>(t.exp_avg), i, n, vec, m);
+      store_e4m3(static_cast<uint8_t*>(t.exp_avg_sq), i, n, vec, root);
       if ((threadIdx.x & 31) == 0) {
         t.m_scale[first / ADAM_BLOCK] = ms;
         t.v_scale[first / ADAM_BLOCK] = vs;

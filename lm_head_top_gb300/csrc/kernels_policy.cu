@@ -2,21 +2,27 @@
 // gradients: the clipped policy loss with a KL term, and the preference loss
 // over pairs of sequences.
 //
-// Tokens lie in one array; sequence s is [cu[s], cu[s+1]). A thread block takes
-// SEQ_CHUNK consecutive tokens, whatever sequences they belong to, so ragged
-// lengths leave no block idle and a long sequence is spread over many blocks.
-// Where a sum per sequence is needed, block b writes its part of sequence s
-// to slot b + s: walking along the tokens either the block or the sequence
-// advances, so no two pairs (b, s) share a slot and blocks + sequences slots
-// hold them all. Sums are joined in a fixed order (no floating-point atomics):
-// the results do not change from run to run.
+// Tokens lie in one array; sequence s is [cu[s], cu[s+1]). The unit of work is a
+// warp and a run of consecutive tokens, whatever sequences they belong to:
+// ragged lengths leave no warp idle and a long sequence is spread over many. A
+// warp walks its run in pieces of 128 tokens, four per lane, and keeps its
+// place among the sequences as it goes, so that finding a token's sequence costs
+// one search per run. Nothing in the walk waits for the other warps of the block.
+// Where a sum per sequence is needed, warp w writes its part of sequence s to
+// slot w + s: along the tokens either the warp or the sequence advances, so no
+// two pairs (w, s) share a slot, and warps + sequences slots hold them all. Sums
+// are joined in a fixed order (no floating-point atomics): the results do not
+// change from run to run.
 //
-// What bounds both on long batches: DRAM (21 bytes a token for the policy loss
-// with per-token advantages, 13 for the preference loss, whose gradient pass
-// reads the mask once more). On short ones: the launches.
+// What bounds both on long batches: DRAM (17 bytes a token for the policy loss
+// with per-sequence advantages, 13 for the preference loss, whose gradient pass
+// reads the mask once more). On short ones: the launches, so a batch that one
+// block can hold takes one launch.
 #include <cuda_bf16.h>
 #include <math.h>
 #include <stdint.h>
+
+#include <algorithm>
 
 #include "kdkl_internal.h"
 #include "tc_primitives.cuh"
@@ -26,8 +32,11 @@ namespace kdkl {
 namespace {
 
 constexpr int SEQ_THREADS = 256;
-constexpr int SEQ_TOK = 8;  // consecutive tokens per thread
-constexpr int SEQ_CHUNK = SEQ_THREADS * SEQ_TOK;
+constexpr int SEQ_WARPS = SEQ_THREADS / 32;
+constexpr int SEQ_TOK = 4;              // consecutive tokens per lane: a 16-byte load
+constexpr int SEQ_PIECE = 32 * SEQ_TOK;  // tokens of a warp's step
+constexpr int SEQ_RESIDENT = 5;          // blocks of a walk on an SM
+constexpr int PREF_ONE_THREADS = 512;   // the one-block preference loss
 
 // First sequence in [lo, lo + n) whose end is past token t (the last one if
 // none is), found by the whole warp: 32 probes a step.
@@ -45,8 +54,16 @@ __device__ __forceinline__ int seq_find_warp(const int32_t* cu, int lo, int n, i
   return min(lo, last);
 }
 
-// The same by one thread.
-__device__ __forceinline__ int seq_find(const int32_t* cu, int lo, int last, int t) {
+// First sequence from s on whose end is past token t (the last one if none
+// is), by one thread: steps that double, then bisection.
+__device__ __noinline__ int seq_advance(const int32_t* cu, int S, int s, int t) {
+  if (s >= S - 1 || __ldg(cu + s + 1) > t) return min(s, S - 1);
+  int lo = s + 1, step = 1;
+  while (lo + step < S && __ldg(cu + lo + step) <= t) {
+    lo += step;
+    step <<= 1;
+  }
+  int last = min(lo + step - 1, S - 1);
   while (lo < last) {
     const int mid = (lo + last) >> 1;
     if (__ldg(cu + mid + 1) <= t) lo = mid + 1; else last = mid;
@@ -54,38 +71,22 @@ __device__ __forceinline__ int seq_find(const int32_t* cu, int lo, int last, int
   return lo;
 }
 
-// Sequences of the block's first and last token, to every thread.
-__device__ __forceinline__ void block_range(const int32_t* cu, int S, int t0, int t1, int* range,
-                                            int& s_lo, int& s_hi) {
-  const int warp = threadIdx.x >> 5;
-  if (warp < 2) {
-    const int s = seq_find_warp(cu, 0, S, warp == 0 ? t0 : t1 - 1);
-    if ((threadIdx.x & 31) == 0) range[warp] = s;
-  }
-  __syncthreads();
-  s_lo = range[0];
-  s_hi = max(range[0], range[1]);
-}
-
-// Eight consecutive values from token t on; those at or past T read as zero.
-__device__ __forceinline__ void load_f8(const float* p, int t, int T, bool vec,
-                                        float (&x)[SEQ_TOK]) {
+// A lane's consecutive values from token t on; those at or past T read as zero.
+__device__ __forceinline__ void load_tok(const float* p, int t, int T, bool vec,
+                                         float (&x)[SEQ_TOK]) {
   if (vec && t + SEQ_TOK <= T) {
     const float4 a = __ldg(reinterpret_cast<const float4*>(p + t));
-    const float4 b = __ldg(reinterpret_cast<const float4*>(p + t) + 1);
     x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
   } else {
 #pragma unroll
     for (int j = 0; j < SEQ_TOK; ++j) x[j] = t + j < T ? __ldg(p + t + j) : 0.f;
   }
 }
 
-__device__ __forceinline__ void store_f8(float* p, int t, int T, bool vec,
-                                         const float (&x)[SEQ_TOK]) {
+__device__ __forceinline__ void store_tok(float* p, int t, int T, bool vec,
+                                          const float (&x)[SEQ_TOK]) {
   if (vec && t + SEQ_TOK <= T) {
     *reinterpret_cast<float4*>(p + t) = make_float4(x[0], x[1], x[2], x[3]);
-    *(reinterpret_cast<float4*>(p + t) + 1) = make_float4(x[4], x[5], x[6], x[7]);
   } else {
 #pragma unroll
     for (int j = 0; j < SEQ_TOK; ++j)
@@ -93,54 +94,39 @@ __device__ __forceinline__ void store_f8(float* p, int t, int T, bool vec,
   }
 }
 
-// Bit j: token t + j exists and counts.
-__device__ __forceinline__ uint32_t load_mask8(const uint8_t* mask, int t, int T, bool vec) {
+// Bit j: byte j of the word is not zero. Each byte's bits are folded onto its
+// lowest (what a shift brings in from the byte above lands on bits not used
+// again), and a product brings the four lowest bits together.
+__device__ __forceinline__ uint32_t nonzero_bytes(uint32_t x) {
+  x |= x >> 4;
+  x |= x >> 2;
+  x |= x >> 1;
+  return ((x & 0x01010101u) * 0x10204080u) >> 28;
+}
+
+// Bit j: token t + j exists and counts, for a lane's tokens.
+__device__ __forceinline__ uint32_t load_mask(const uint8_t* mask, int t, int T, bool vec) {
+  if (mask == nullptr)
+    return t + SEQ_TOK <= T ? (1u << SEQ_TOK) - 1u : t < T ? (1u << (T - t)) - 1u : 0u;
+  if (vec && t + SEQ_TOK <= T)
+    return nonzero_bytes(__ldg(reinterpret_cast<const uint32_t*>(mask + t)));
   uint32_t on = 0;
-  if (mask == nullptr) {
-#pragma unroll
-    for (int j = 0; j < SEQ_TOK; ++j) on |= (t + j < T ? 1u : 0u) << j;
-  } else if (vec && t + SEQ_TOK <= T) {
-    const uint2 w = __ldg(reinterpret_cast<const uint2*>(mask + t));
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      on |= ((w.x >> (8 * j)) & 0xffu ? 1u : 0u) << j;
-      on |= ((w.y >> (8 * j)) & 0xffu ? 1u : 0u) << (4 + j);
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < SEQ_TOK; ++j) on |= (t + j < T && __ldg(mask + t + j) != 0 ? 1u : 0u) << j;
-  }
+#pragma unroll 1
+  for (int j = 0; j < SEQ_TOK && t + j < T; ++j) on |= (__ldg(mask + t + j) != 0 ? 1u : 0u) << j;
   return on;
 }
 
-template <typename T>
-__device__ __forceinline__ T warp_sum(T v) {
+// The same for 16 tokens.
+__device__ __forceinline__ uint32_t load_mask16(const uint8_t* mask, int t, int T, bool vec) {
+  if (mask && vec && t + 16 <= T) {
+    const uint4 w = __ldg(reinterpret_cast<const uint4*>(mask + t));
+    return nonzero_bytes(w.x) | nonzero_bytes(w.y) << 4 | nonzero_bytes(w.z) << 8 |
+           nonzero_bytes(w.w) << 12;
+  }
+  uint32_t on = 0;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
-// Sum over the block in a fixed order, valid in thread 0.
-template <typename T>
-__device__ __forceinline__ T block_sum(T v, T* part) {
-  v = warp_sum(v);
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-  __syncthreads();
-  T r = 0;
-  if (threadIdx.x == 0)
-    for (int i = 0; i < (int)blockDim.x / 32; ++i) r += part[i];
-  __syncthreads();
-  return r;
-}
-
-// True in every thread of the block that finishes last.
-__device__ __forceinline__ bool last_block(int* ticket, int* flag) {
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) *flag = atomicAdd(ticket, 1) == (int)gridDim.x - 1;
-  __syncthreads();
-  if (*flag) __threadfence();
-  return *flag != 0;
+  for (int k = 0; k < 16; k += SEQ_TOK) on |= load_mask(mask, t + k, T, vec) << k;
+  return on;
 }
 
 // cu must start at 0, end at T and never fall.
@@ -153,73 +139,138 @@ __device__ __forceinline__ void check_cu(const int32_t* cu, int S, int T, int* s
   }
 }
 
+// A sum in two floats: each addition's rounding error is kept, 48 bits in all.
+// The fp64 unit here takes 16 cycles for a warp's addition: joining the warps'
+// sums in fp64 alone cost the policy loss 4 us whatever its length.
+struct Sum2 {
+  float hi = 0.f, lo = 0.f;
+  __device__ __forceinline__ void add(float x, float x_lo = 0.f) {
+    const float t = hi + x, b = t - hi;
+    lo += ((hi - (t - b)) + (x - b)) + x_lo;
+    hi = t;
+  }
+  // (an infinite sum has no error term)
+  __device__ __forceinline__ float value() const { return lo == lo ? hi + lo : hi; }
+};
+
+// Lane 0 has the warp's sum, in a fixed order.
+__device__ __forceinline__ Sum2 warp_sum(Sum2 v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float hi = __shfl_down_sync(0xffffffffu, v.hi, o);
+    const float lo = __shfl_down_sync(0xffffffffu, v.lo, o);
+    v.add(hi, lo);
+  }
+  return v;
+}
+
+// Tokens of one warp's run when `warps` of them share T tokens.
+__device__ __forceinline__ int run_length(int T, int warps) {
+  return (int)(((long long)T + (long long)warps * SEQ_PIECE - 1) /
+               ((long long)warps * SEQ_PIECE)) * SEQ_PIECE;
+}
+
+// Launches that follow one another closely: the next one's blocks may start
+// (up to their wait) while this one runs.
+__device__ __forceinline__ void grid_dependents_go() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+// Waits until the launches before this one are complete and their writes seen.
+__device__ __forceinline__ void grid_dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
 // --------------------------------------------------------------- policy loss
 
-// Counted tokens: of all (n_seq == nullptr) into n_count[0], or of every
-// sequence into n_seq[s], and then into n_count[1] how many have any. Whole
-// numbers, so atomics give the same answer in any order.
+// Counted tokens: of all into n_count[0]; with n_seq, of every sequence into
+// n_seq[s], and how many sequences have any into n_count[1] (whoever finds a
+// sequence's count at zero counts it). Whole numbers, so atomics give the same
+// answer in any order.
 __global__ void __launch_bounds__(SEQ_THREADS)
     policy_count_kernel(const uint8_t* __restrict__ mask, const int32_t* __restrict__ cu, int T,
-                        int S, int vec, int* __restrict__ n_seq, int* __restrict__ n_count,
-                        int* __restrict__ ticket) {
-  __shared__ int range[2], part[SEQ_THREADS / 32], flag;
-  const int t0 = blockIdx.x * SEQ_CHUNK;
-  const int t1 = min(T, t0 + SEQ_CHUNK);
-  const int t = t0 + threadIdx.x * SEQ_TOK;
-  const uint32_t on = load_mask8(mask, t, T, vec != 0);
-  const int all = block_sum(__popc(on), part);
-  if (threadIdx.x == 0 && all) atomicAdd(n_count, all);
-  if (n_seq == nullptr) return;
-  int s_lo, s_hi;
-  block_range(cu, S, t0, t1, range, s_lo, s_hi);
-  if (s_lo == s_hi) {
-    if (threadIdx.x == 0 && all) atomicAdd(n_seq + s_lo, all);
-  } else if (t < t1) {
-    int s = seq_find(cu, s_lo, s_hi, t);
-    int run = 0;
-#pragma unroll
-    for (int j = 0; j < SEQ_TOK; ++j) {
-      while (s < s_hi && t + j >= __ldg(cu + s + 1)) {
-        if (run) atomicAdd(n_seq + s, run);
-        run = 0;
-        ++s;
-      }
-      run += (on >> j) & 1u;
+                        int S, int vec, int* __restrict__ n_seq, int* __restrict__ n_count) {
+  __shared__ int block_count;
+  grid_dependents_go();
+  if (threadIdx.x == 0) block_count = 0;
+  __syncthreads();
+  const int lane = threadIdx.x & 31;
+  constexpr int TOK = 16, PIECE = 32 * TOK;  // per lane and step here
+  const int R = (run_length(T, (int)gridDim.x * SEQ_WARPS) + PIECE - 1) / PIECE * PIECE;
+  const long long first = (long long)(blockIdx.x * SEQ_WARPS + (threadIdx.x >> 5)) * R;
+  const int run_end = (int)min((long long)T, first + R);
+  // the whole run's mask is on its way while the first sequence is looked for
+  if (mask)
+    for (long long i = first + lane * 128; i < run_end; i += 32 * 128) prefetch_l2(mask + i);
+  auto put = [&](int s, int c) {
+    if (c && atomicAdd(n_seq + s, c) == 0) atomicAdd(n_count + 1, 1);
+  };
+  int total = 0;
+  int s = 0, end = -1;
+  if (n_seq && first < T) s = seq_find_warp(cu, 0, S, (int)first);
+  for (int p = (int)min((long long)T, first); p < run_end; p += PIECE) {
+    const int t = p + lane * TOK;
+    const uint32_t on = load_mask16(mask, t, T, vec != 0);
+    const int c = __popc(on);
+    total += c;
+    if (n_seq == nullptr) continue;
+    if (t < run_end && t >= end) {
+      s = seq_advance(cu, S, s, t);
+      end = s < S - 1 ? __ldg(cu + s + 1) : T;
     }
-    if (run) atomicAdd(n_seq + s, run);
+    const int s0 = __shfl_sync(0xffffffffu, s, 0);
+    if (__all_sync(0xffffffffu, t >= run_end || (s == s0 && min(t + TOK, T) <= end))) {
+      const int all = __reduce_add_sync(0xffffffffu, c);
+      if (lane == 0) put(s0, all);
+    } else if (t < run_end) {
+      int at = 0;  // the lane's tokens from here on are not put yet
+      while (end < t + TOK && s < S - 1) {
+        const int upto = max(at, end - t);
+        put(s, __popc(on & ((1u << upto) - 1u) & ~((1u << at) - 1u)));
+        at = upto;
+        if (t + at >= T) break;
+        s = seq_advance(cu, S, s, t + at);
+        end = s < S - 1 ? __ldg(cu + s + 1) : T;
+      }
+      put(s, __popc(on & ~((1u << at) - 1u)));
+    }
   }
-  if (!last_block(ticket, &flag)) return;
-  int any = 0;
-  for (int s = threadIdx.x; s < S; s += SEQ_THREADS) any += __ldcg(n_seq + s) > 0 ? 1 : 0;
-  any = block_sum(any, part);
-  if (threadIdx.x == 0) n_count[1] = any;
+  total = __reduce_add_sync(0xffffffffu, total);
+  if (lane == 0 && total) atomicAdd(&block_count, total);
+  __syncthreads();
+  if (threadIdx.x == 0 && block_count) atomicAdd(n_count, block_count);
 }
 
-// a - b against a border that takes 64 bits: the difference of two floats is
-// the rounded one plus an error that is a float too, and the border is held
-// the same way, as a float and a remainder.
-__device__ __forceinline__ bool exceeds(float d, float e, float hi, float lo) {
-  return d > hi || (d == hi && e > lo);
+// Whether p - q exceeds a border that takes 64 bits. d is the difference
+// rounded to a float, the border a float and a remainder. Rounding is monotone,
+// so d decides unless it is the border's own float (hardly ever): then the
+// rounding error of d, which is a float too, is held against the remainder.
+__device__ __forceinline__ bool exceeds(float d, float p, float q, float hi, float lo) {
+  bool over = d > hi;
+  if (d == hi) {
+    const float b = d - p;
+    over = (p - (d - b)) - (q + b) > lo;
+  }
+  return over;
 }
 
-// e^x - 1 - x without its cancellation near 0: for |x| < 1 the power series
-// x^2 (1/2! + x/3! + ... + x^10/12!), whose next term is below 2^-29 of the sum.
+// e^x by the hardware's base-2 exponential: 2 ulp and the rounding of x log2(e).
+__device__ __forceinline__ float exp_fast(float x) { return ex2_approx(x * 1.4426950408889634f); }
+
+// e^x - 1 - x without its cancellation near 0: for |x| < 0.35 the power series
+// x^2 (1/2! + x/3! + ... + x^6/8!), whose next term is below 2^-27 of the sum.
 __device__ __forceinline__ float exp_rest(float x) {
-  if (fabsf(x) < 1.f) {
-    float p = 1.f / 479001600.f;
-    p = fmaf(p, x, 1.f / 39916800.f);
-    p = fmaf(p, x, 1.f / 3628800.f);
-    p = fmaf(p, x, 1.f / 362880.f);
-    p = fmaf(p, x, 1.f / 40320.f);
-    p = fmaf(p, x, 1.f / 5040.f);
-    p = fmaf(p, x, 1.f / 720.f);
-    p = fmaf(p, x, 1.f / 120.f);
-    p = fmaf(p, x, 1.f / 24.f);
-    p = fmaf(p, x, 1.f / 6.f);
-    p = fmaf(p, x, 0.5f);
-    return p * x * x;
-  }
-  return (expf(x) - 1.f) - x;
+  float p = 1.f / 40320.f;
+  p = fmaf(p, x, 1.f / 5040.f);
+  p = fmaf(p, x, 1.f / 720.f);
+  p = fmaf(p, x, 1.f / 120.f);
+  p = fmaf(p, x, 1.f / 24.f);
+  p = fmaf(p, x, 1.f / 6.f);
+  p = fmaf(p, x, 0.5f);
+  const float far = (exp_fast(x) - 1.f) - x;
+  return fabsf(x) < 0.35f ? p * x * x : far;
 }
 
 // One pass over the tokens: ratio, clip, KL term, gradient, and per block the
@@ -227,309 +278,440 @@ __device__ __forceinline__ float exp_rest(float x) {
 // the block that finishes last joins the blocks' sums.
 //   NEED_SEQ: a token's sequence is looked up (advantages or weights per sequence).
 template <bool NEED_SEQ>
-__global__ void __launch_bounds__(SEQ_THREADS)
+__global__ void __launch_bounds__(SEQ_THREADS, SEQ_RESIDENT)
     policy_loss_kernel(const PolicyArgs a, int* status) {
-  __shared__ int range[2], ipart[SEQ_THREADS / 32], flag;
-  __shared__ double part[SEQ_THREADS / 32];
-  const int t0 = blockIdx.x * SEQ_CHUNK;
-  const int t1 = min(a.T, t0 + SEQ_CHUNK);
-  const int t = t0 + threadIdx.x * SEQ_TOK;
+  __shared__ int count, clips;
+  __shared__ float2 part[2][SEQ_WARPS];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool alone = gridDim.x == 1;
   const bool vec = a.vec != 0;
-  const uint32_t on = load_mask8(a.mask, t, a.T, vec);
-  float lp[SEQ_TOK], lo[SEQ_TOK], lr[SEQ_TOK], adv[SEQ_TOK];
-  load_f8(a.logp, t, a.T, vec, lp);
-  if (a.old_logp) load_f8(a.old_logp, t, a.T, vec, lo);
-  if (a.ref_logp) load_f8(a.ref_logp, t, a.T, vec, lr);
-  if (!a.adv_per_seq) load_f8(a.advantages, t, a.T, vec, adv);
-
-  int s = 0, s_hi = 0;
-  if (NEED_SEQ) {
-    check_cu(a.cu, a.S, a.T, status);
-    int s_lo;
-    block_range(a.cu, a.S, t0, t1, range, s_lo, s_hi);
-    s = t < t1 ? seq_find(a.cu, s_lo, s_hi, t) : s_hi;
+  if (threadIdx.x == 0) {
+    count = clips = 0;
+    if (alone) *status = 0;  // with more blocks the call has cleared it
   }
+  __syncthreads();
+  const int R = run_length(a.T, (int)gridDim.x * SEQ_WARPS);
+  const long long first = (long long)(blockIdx.x * SEQ_WARPS + warp) * R;
+  const int begin = (int)min((long long)a.T, first);
+  const int run_end = (int)min((long long)a.T, first + R);
+
+  if (lane < 8 && begin + lane * 32 < run_end) {  // two pieces are on their way during the lookups
+    prefetch_l2(a.logp + begin + lane * 32);
+    if (a.old_logp) prefetch_l2(a.old_logp + begin + lane * 32);
+    if (a.ref_logp) prefetch_l2(a.ref_logp + begin + lane * 32);
+  }
+  int s = 0, end = a.T;
+  if (NEED_SEQ && begin < run_end) s = seq_find_warp(a.cu, 0, a.S, begin);
+  grid_dependency_wait();  // the counts, and the cleared status
+  if (NEED_SEQ) check_cu(a.cu, a.S, a.T, status);
   // Counted tokens: given (no mask), counted before, or counted here by every
   // block for itself (a short mask, which saves the launch that would count it).
   int n = a.T;
   if (a.mask) {
     if (a.count_here) {
       int c = 0;
-      for (int i = threadIdx.x * SEQ_TOK; i < a.T; i += SEQ_CHUNK)
-        c += __popc(load_mask8(a.mask, i, a.T, vec));
-      c = block_sum(c, ipart);
-      if (threadIdx.x == 0) range[0] = c;
+      for (int i = threadIdx.x * 16; i < a.T; i += SEQ_THREADS * 16)
+        c += __popc(load_mask16(a.mask, i, a.T, vec));
+      c = __reduce_add_sync(0xffffffffu, c);
+      if (lane == 0 && c) atomicAdd(&count, c);
       __syncthreads();
-      n = range[0];
+      n = count;
     } else {
-      n = *a.n_count;
+      n = __ldcg(a.n_count);
     }
   }
-  const int n_any = a.reduction == 1 ? a.n_count[1] : 0;
+  const int n_any = a.reduction == 1 ? __ldcg(a.n_count + 1) : 0;
   float w = a.reduction == 0 ? (n > 0 ? 1.f / (float)n : 0.f) : a.inv_norm;
   float w_adv = 0.f;  // the sequence's advantage
-  auto enter = [&]() {  // the sequence's values
+  auto enter = [&](int t) {  // the sequence of token t and its values
+    s = seq_advance(a.cu, a.S, s, t);
+    end = s < a.S - 1 ? __ldg(a.cu + s + 1) : a.T;
     if (a.adv_per_seq) w_adv = __ldg(a.advantages + s);
     if (a.reduction == 1) {
-      const int ns = __ldg(a.n_seq + s);
+      const int ns = __ldcg(a.n_seq + s);
       w = ns > 0 ? 1.f / ((float)ns * (float)n_any) : 0.f;
     }
   };
-  if (NEED_SEQ) enter();
+  if (NEED_SEQ) end = -1;  // enter at the first token
 
-  float g[SEQ_TOK];
-  float pg = 0.f, kl = 0.f;
+  const float* ahead = lane < 4 ? a.logp : lane < 8 ? a.old_logp : lane < 12 ? a.ref_logp : nullptr;
+  if (lane >= 12 && lane < 16 && !a.adv_per_seq) ahead = a.advantages;
+  Sum2 pg, kl;
   int clipped = 0;
+  for (int p = begin; p < run_end; p += SEQ_PIECE) {
+    const int t = p + lane * SEQ_TOK;
+    // a lane per line of a piece's arrays: the piece after the next one's way
+    // from memory starts two steps before it is needed
+    if (ahead && p + 2 * SEQ_PIECE + (lane & 3) * 32 < run_end)
+      prefetch_l2(ahead + p + 2 * SEQ_PIECE + (lane & 3) * 32);
+    if (t >= run_end) break;  // nothing below is collective
+    const uint32_t on = load_mask(a.mask, t, a.T, vec);
+    float lp[SEQ_TOK], lo[SEQ_TOK], lr[SEQ_TOK], adv[SEQ_TOK];
+    load_tok(a.logp, t, a.T, vec, lp);
+    if (a.old_logp) load_tok(a.old_logp, t, a.T, vec, lo);
+    if (a.ref_logp) load_tok(a.ref_logp, t, a.T, vec, lr);
+    if (!a.adv_per_seq) load_tok(a.advantages, t, a.T, vec, adv);
+    float g[SEQ_TOK];
 #pragma unroll
-  for (int j = 0; j < SEQ_TOK; ++j) {
-    if (NEED_SEQ) {
-      bool moved = false;
-      while (s < s_hi && t + j >= __ldg(a.cu + s + 1)) {
-        ++s;
-        moved = true;
+    for (int j = 0; j < SEQ_TOK; ++j) g[j] = 0.f;
+    float pg1 = 0.f, kl1 = 0.f;
+    // The lane's tokens, a sequence at a time: once, but where one ends.
+    for (int at = t; at < min(t + SEQ_TOK, a.T);) {
+      uint32_t mine = on;
+      int upto = t + SEQ_TOK;
+      if (NEED_SEQ) {
+        if (at >= end) enter(at);
+        // (an end that is not past `at` comes of bad offsets: the last sequence's then)
+        if (end > at && end < upto) upto = end;
+        mine &= ((1u << (upto - t)) - 1u) & ~((1u << (at - t)) - 1u);
       }
-      if (moved) enter();
+      at = upto;
+#pragma unroll
+      for (int j = 0; j < SEQ_TOK; ++j) {
+        // What lies under the mask is replaced before it is used: d = 0 is inside
+        // every border, and the advantage and the weight are zero.
+        const bool counts = (mine >> j) & 1u;
+        const float A = counts ? (a.adv_per_seq ? w_adv : adv[j]) : 0.f;
+        const float wj = counts ? w : 0.f;
+        const bool pos = A >= 0.f;
+        float r = 1.f;
+        bool clip = false;
+        if (a.old_logp) {
+          const float d = counts ? lp[j] - lo[j] : 0.f;
+          const float side = pos ? d : -d, border = pos ? a.high_hi : -a.low_hi;
+          clip = side > border;
+          if (side == border)  // hardly ever
+            clip = pos ? exceeds(d, lp[j], lo[j], a.high_hi, a.high_lo)
+                       : exceeds(-d, lo[j], lp[j], -a.low_hi, -a.low_lo);
+          r = clip ? (pos ? a.r_high : a.r_low) : exp_fast(d);
+          if (a.dual && !pos && d >= a.dual_hi && exceeds(d, lp[j], lo[j], a.dual_hi, a.dual_lo)) {
+            clip = true;
+            r = a.r_dual;
+          }
+        }
+        const float rA = r * A;
+        pg1 = fmaf(-wj, rA, pg1);
+        float gj = clip ? 0.f : -rA;
+        if (a.ref_logp) {
+          const float x = counts ? lr[j] - lp[j] : 0.f;
+          const float k = exp_rest(x);
+          kl1 = fmaf(wj, k, kl1);
+          gj = fmaf(-a.kl_coef, x + k, gj);
+        }
+        clipped += clip ? 1 : 0;
+        g[j] = fmaf(wj * a.grad_loss, gj, g[j]);
+      }
     }
-    g[j] = 0.f;
-    if ((on >> j) & 1u) {  // what lies under the mask is never used
-      const float A = a.adv_per_seq ? w_adv : adv[j];
-      float d = 0.f, e = 0.f;
-      if (a.old_logp) {
-        d = lp[j] - lo[j];
-        const float bb = d - lp[j];
-        e = (lp[j] - (d - bb)) - (lo[j] + bb);
-      }
-      const bool pos = A >= 0.f;
-      float bound = pos ? a.r_high : a.r_low;
-      bool clip = pos ? exceeds(d, e, a.high_hi, a.high_lo)
-                      : exceeds(-d, -e, -a.low_hi, -a.low_lo);
-      if (a.dual && !pos && exceeds(d, e, a.dual_hi, a.dual_lo)) {
-        clip = true;
-        bound = a.r_dual;
-      }
-      const float r = clip ? bound : expf(d);
-      pg = fmaf(-w * r, A, pg);
-      float gj = clip ? 0.f : -r * A;
-      if (a.ref_logp) {
-        const float x = lr[j] - lp[j];
-        const float k = exp_rest(x);
-        kl = fmaf(w, k, kl);
-        gj -= a.kl_coef * (x + k);
-      }
-      g[j] = w * gj * a.grad_loss;
-      clipped += clip ? 1 : 0;
+    if (a.grad) store_tok(a.grad, t, a.T, vec, g);
+    pg.add(pg1);
+    kl.add(kl1);
+  }
+  __syncwarp();
+  pg = warp_sum(pg);
+  kl = warp_sum(kl);
+  clipped = __reduce_add_sync(0xffffffffu, clipped);
+  if (lane == 0) {
+    part[0][warp] = make_float2(pg.hi, pg.lo);
+    part[1][warp] = make_float2(kl.hi, kl.lo);
+    if (clipped) atomicAdd(&clips, clipped);
+  }
+  __syncthreads();
+  if (warp != 0) return;
+  // Warp 0: the block's sums (lanes 0 to 7 hold the warps'), then, in the block
+  // that finishes last, all blocks'.
+  auto load = [](const float2& v) {
+    Sum2 r;
+    r.hi = v.x;
+    r.lo = v.y;
+    return r;
+  };
+  pg = lane < SEQ_WARPS ? load(part[0][lane]) : Sum2();
+  kl = lane < SEQ_WARPS ? load(part[1][lane]) : Sum2();
+  pg = warp_sum(pg);
+  kl = warp_sum(kl);
+  clipped = clips;
+  if (!alone) {
+    int done = 0;
+    if (lane == 0) {
+      a.block_part[blockIdx.x] = make_float4(pg.hi, pg.lo, kl.hi, kl.lo);
+      if (clipped) atomicAdd(a.n_count + 2, clipped);
+      __threadfence();
+      done = atomicAdd(a.ticket, 1) == (int)gridDim.x - 1;
     }
+    if (!__shfl_sync(0xffffffffu, done, 0)) return;
+    __threadfence();
+    pg = kl = Sum2();
+#pragma unroll 8
+    for (int b = lane; b < (int)gridDim.x; b += 32) {
+      const float4 v = __ldcg(a.block_part + b);
+      pg.add(v.x, v.y);
+      kl.add(v.z, v.w);
+    }
+    pg = warp_sum(pg);
+    kl = warp_sum(kl);
+    clipped = __ldcg(a.n_count + 2);
   }
-  if (a.grad && t < t1) store_f8(a.grad, t, a.T, vec, g);
-
-  const double spg = block_sum((double)pg, part);
-  const double skl = block_sum((double)kl, part);
-  const int scl = block_sum(clipped, ipart);
-  if (threadIdx.x == 0) {
-    a.block_part[3 * (long long)blockIdx.x] = spg;
-    a.block_part[3 * (long long)blockIdx.x + 1] = skl;
-    a.block_part[3 * (long long)blockIdx.x + 2] = (double)scl;
-  }
-  if (!last_block(a.ticket, &flag)) return;
-  double v[3] = {0.0, 0.0, 0.0};
-  for (int b = threadIdx.x; b < (int)gridDim.x; b += SEQ_THREADS)
-#pragma unroll
-    for (int q = 0; q < 3; ++q) v[q] += __ldcg(a.block_part + 3 * (long long)b + q);
-#pragma unroll
-  for (int q = 0; q < 3; ++q) v[q] = block_sum(v[q], part);
-  if (threadIdx.x == 0) {
-    a.loss[0] = (float)(v[0] + (double)a.kl_coef * v[1]);
+  if (lane == 0) {
+    Sum2 loss = pg;
+    loss.add(a.kl_coef * kl.hi, a.kl_coef * kl.lo);
+    a.loss[0] = loss.value();
     if (a.stats) {
-      a.stats[0] = (float)v[0];
-      a.stats[1] = (float)v[1];
-      a.stats[2] = n > 0 ? (float)(v[2] / (double)n) : 0.f;
+      a.stats[0] = pg.value();
+      a.stats[1] = kl.value();
+      a.stats[2] = n > 0 ? (float)clipped / (float)n : 0.f;
     }
   }
 }
 
 // ----------------------------------------------------------- preference loss
 
-// Block b's part of every sequence s that it meets, to slot b + s: the sum of
+// Warp w's part of every sequence s that it meets, to slot w + s: the sum of
 // the counted tokens' log ratios, and how many they are.
-__global__ void __launch_bounds__(SEQ_THREADS)
-    pref_sums_kernel(const float* __restrict__ logp, const float* __restrict__ ref,
-                     const uint8_t* __restrict__ mask, const int32_t* __restrict__ cu, int T, int S,
-                     int vec, double* __restrict__ slot_sum, int* __restrict__ slot_n,
-                     int* __restrict__ status) {
-  __shared__ int range[2], ipart[SEQ_THREADS / 32];
-  __shared__ double part[SEQ_THREADS / 32];
-  __shared__ float gap[SEQ_CHUNK];
-  __shared__ uint8_t cnt[SEQ_CHUNK];
-  const int t0 = blockIdx.x * SEQ_CHUNK;
-  const int t1 = min(T, t0 + SEQ_CHUNK);
-  const int t = t0 + threadIdx.x * SEQ_TOK;
-  const uint32_t on = load_mask8(mask, t, T, vec != 0);
-  float x[SEQ_TOK], y[SEQ_TOK];
-  load_f8(logp, t, T, vec != 0, x);
-  if (ref) load_f8(ref, t, T, vec != 0, y);
-  check_cu(cu, S, T, status);
-  int s_lo, s_hi;
-  block_range(cu, S, t0, t1, range, s_lo, s_hi);
-#pragma unroll
-  for (int j = 0; j < SEQ_TOK; ++j)
-    x[j] = (on >> j) & 1u ? (ref ? x[j] - y[j] : x[j]) : 0.f;
-  if (s_lo == s_hi) {
-    float sum = 0.f;
-#pragma unroll
-    for (int j = 0; j < SEQ_TOK; ++j) sum += x[j];
-    const double all = block_sum((double)sum, part);
-    const int n = block_sum(__popc(on), ipart);
-    if (threadIdx.x == 0) {
-      slot_sum[(long long)blockIdx.x + s_lo] = all;
-      slot_n[(long long)blockIdx.x + s_lo] = n;
-    }
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < SEQ_TOK; ++j) {
-    gap[threadIdx.x * SEQ_TOK + j] = x[j];
-    cnt[threadIdx.x * SEQ_TOK + j] = (uint8_t)((on >> j) & 1u);
-  }
-  __syncthreads();
-  // a warp per sequence, its lanes across the sequence's tokens
+__device__ __forceinline__ void pref_sums(const PrefArgs& a, int w, int R) {
   const int lane = threadIdx.x & 31;
-  for (int s = s_lo + (threadIdx.x >> 5); s <= s_hi; s += SEQ_THREADS / 32) {
-    const int a = max(__ldg(cu + s), t0) - t0, b = min(__ldg(cu + s + 1), t1) - t0;
-    float sum = 0.f;
-    int n = 0;
-    for (int i = a + lane; i < b; i += 32) {
-      sum += gap[i];
-      n += cnt[i];
-    }
-    const double all = warp_sum((double)sum);
-    n = warp_sum(n);
+  const int S = 2 * a.P;
+  const long long first = (long long)w * R;
+  if (first >= a.T) return;
+  const int run_end = (int)min((long long)a.T, first + R);
+  int s = seq_find_warp(a.cu, 0, S, (int)first);
+  int end = s < S - 1 ? __ldg(a.cu + s + 1) : a.T;  // uniform, as s
+  Sum2 sum;
+  int n = 0;
+  auto flush = [&]() {
+    sum = warp_sum(sum);
+    const int c = __reduce_add_sync(0xffffffffu, n);
     if (lane == 0) {
-      slot_sum[(long long)blockIdx.x + s] = all;
-      slot_n[(long long)blockIdx.x + s] = n;
+      a.slot_sum[(long long)w + s] = make_float2(sum.hi, sum.lo);
+      a.slot_n[(long long)w + s] = c;
     }
-  }
-}
-
-// A warp per pair: both sequences' sums from their slots, the pair's loss, and
-// the gradient that each counted token of either sequence gets.
-__global__ void __launch_bounds__(SEQ_THREADS) pref_pairs_kernel(const PrefArgs a) {
-  __shared__ int flag;
-  __shared__ double part[SEQ_THREADS / 32];
-  const int lane = threadIdx.x & 31;
-  const int i = blockIdx.x * (SEQ_THREADS / 32) + (threadIdx.x >> 5);
-  if (i < a.P) {
-    int seq[2] = {a.halves ? i : 2 * i, a.halves ? a.P + i : 2 * i + 1};
-    double ratio[2], share[2];
+    sum = Sum2();
+    n = 0;
+  };
+  for (int p = (int)first; p < run_end; p += SEQ_PIECE) {
+    const int t = p + lane * SEQ_TOK;
+    const uint32_t on = load_mask(a.mask, t, a.T, a.vec != 0);
+    float x[SEQ_TOK], y[SEQ_TOK];
+    load_tok(a.logp, t, a.T, a.vec != 0, x);
+    if (a.ref_logp) load_tok(a.ref_logp, t, a.T, a.vec != 0, y);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int s = seq[k];
-      const int c0 = max(0, min(a.T, __ldg(a.cu + s))), c1 = max(0, min(a.T, __ldg(a.cu + s + 1)));
-      double sum = 0.0;
-      int n = 0;
-      if (c1 > c0)
-        for (int b = c0 / SEQ_CHUNK + lane; b <= (c1 - 1) / SEQ_CHUNK; b += 32) {
-          sum += a.slot_sum[(long long)b + s];
-          n += a.slot_n[(long long)b + s];
-        }
-      sum = warp_sum(sum);
-      n = warp_sum(n);
-      share[k] = a.average ? 1.0 / (double)max(n, 1) : 1.0;
-      ratio[k] = sum * share[k];
-    }
-    if (lane == 0) {
-      const double h = ratio[0] - ratio[1] - a.margin;
-      const double b = a.beta * h, eps = a.label_smoothing;
-      double each, slope;
-      if (a.kind == 0) {
-        // -log sigma(b) = log(1 + e^-|b|) + max(-b, 0); its mirror for -b
-        const double soft = log1p(exp(-fabs(b)));
-        each = (1.0 - eps) * (soft + fmax(-b, 0.0)) + eps * (soft + fmax(b, 0.0));
-        slope = a.beta * (eps - 1.0 / (1.0 + exp(b)));
-      } else if (a.kind == 1) {
-        const double off = h - 0.5 / a.beta;
-        each = off * off;
-        slope = 2.0 * off;
-      } else {
-        each = fmax(1.0 - b, 0.0);
-        slope = b < 1.0 ? -a.beta : 0.0;
+    for (int j = 0; j < SEQ_TOK; ++j)
+      x[j] = (on >> j) & 1u ? (a.ref_logp ? x[j] - y[j] : x[j]) : 0.f;
+    const int piece_end = min(run_end, p + SEQ_PIECE);
+    int at = p;  // tokens of the piece before it have been added
+    while (end < piece_end && s < S - 1) {
+      // the sequence ends inside the piece
+      float part = 0.f;
+#pragma unroll
+      for (int j = 0; j < SEQ_TOK; ++j) {
+        const bool mine = t + j >= at && t + j < end;
+        part += mine ? x[j] : 0.f;
+        n += mine ? (int)((on >> j) & 1u) : 0;
       }
-      if (b != b) each = slope = b;  // fmax drops a NaN
-      a.pair_loss[i] = each;
-      a.rewards[2 * i] = (float)(a.beta * ratio[0]);
-      a.rewards[2 * i + 1] = (float)(a.beta * ratio[1]);
-      slope *= a.grad_loss / (double)a.P;
-      a.coef[seq[0]] = (float)(slope * share[0]);
-      a.coef[seq[1]] = (float)(-slope * share[1]);
+      sum.add(part);
+      flush();
+      at = max(at, end);
+      s = seq_advance(a.cu, S, s, at);
+      end = s < S - 1 ? __ldg(a.cu + s + 1) : a.T;
+    }
+    float part = 0.f;
+#pragma unroll
+    for (int j = 0; j < SEQ_TOK; ++j) {
+      const bool mine = t + j >= at;
+      part += mine ? x[j] : 0.f;
+      n += mine ? (int)((on >> j) & 1u) : 0;
+    }
+    sum.add(part);
+  }
+  flush();
+}
+
+// One warp: both sequences' sums of pair i from their slots, the pair's loss,
+// and the gradient that each counted token of either sequence gets.
+__device__ __forceinline__ void pref_pair(const PrefArgs& a, int i, int R, int* status) {
+  const int lane = threadIdx.x & 31;
+  const int S = 2 * a.P;
+  const int seq[2] = {a.halves ? i : 2 * i, a.halves ? a.P + i : 2 * i + 1};
+  Sum2 q[2];
+  float share[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int s = seq[k];
+    const int b0 = __ldg(a.cu + s), b1 = __ldg(a.cu + s + 1);
+    if (lane == 0 && (b0 > b1 || (s == 0 && b0 != 0) || (s == S - 1 && b1 != a.T)))
+      record_error(status, DEV_ERR_INVALID_ARG);
+    const int c0 = max(0, min(a.T, b0)), c1 = max(0, min(a.T, b1));
+    int n = 0;
+    if (c1 > c0)
+      for (int w = c0 / R + lane; w <= (c1 - 1) / R; w += 32) {
+        const float2 v = a.slot_sum[(long long)w + s];
+        q[k].add(v.x, v.y);
+        n += a.slot_n[(long long)w + s];
+      }
+    q[k] = warp_sum(q[k]);
+    n = __reduce_add_sync(0xffffffffu, n);
+    share[k] = 1.f;
+    if (a.average) {  // the quotient in two floats too: h is a difference of these
+      const float m = (float)max(n, 1);
+      share[k] = 1.f / m;
+      const float hi = q[k].hi / m;
+      q[k].lo = (fmaf(-hi, m, q[k].hi) + q[k].lo) / m;
+      q[k].hi = hi;
     }
   }
-  if (!last_block(a.ticket, &flag)) return;
-  double v = 0.0;
-  for (int p = threadIdx.x; p < a.P; p += SEQ_THREADS) v += __ldcg(a.pair_loss + p);
-  v = block_sum(v, part);
-  if (threadIdx.x == 0) a.loss[0] = (float)(v / (double)a.P);
+  if (lane == 0) {
+    Sum2 gap = q[0];
+    gap.add(-q[1].hi, -q[1].lo);
+    gap.add(-a.margin);
+    const float h = gap.value(), b = a.beta * h, eps = a.label_smoothing;
+    float each, slope;
+    if (a.kind == 0) {
+      // -log sigma(b) = log(1 + e^-|b|) + max(-b, 0), its mirror for -b, and
+      // sigma(-b), from one exponential of -|b|
+      const float e = expf(-fabsf(b)), soft = log1pf(e);
+      each = (1.f - eps) * (soft + fmaxf(-b, 0.f)) + eps * (soft + fmaxf(b, 0.f));
+      slope = a.beta * (eps - (b > 0.f ? e : 1.f) / (1.f + e));
+    } else if (a.kind == 1) {
+      gap.add(-a.half_inv_beta);
+      const float off = gap.value();
+      each = off * off;
+      slope = 2.f * off;
+    } else {
+      each = fmaxf(1.f - b, 0.f);
+      slope = b < 1.f ? -a.beta : 0.f;
+    }
+    if (b != b) each = slope = b;  // fmaxf drops a NaN
+    a.pair_loss[i] = each;
+    a.rewards[2 * i] = a.beta * q[0].value();
+    a.rewards[2 * i + 1] = a.beta * q[1].value();
+    slope *= a.grad_over_P;
+    a.coef[seq[0]] = slope * share[0];
+    a.coef[seq[1]] = -slope * share[1];
+  }
+}
+
+// Every counted token of warp w's run gets its sequence's gradient. coef was
+// written by the launch, or by the part of the block, before.
+__device__ __forceinline__ void pref_grads(const PrefArgs& a, int w, int R) {
+  const int lane = threadIdx.x & 31;
+  const int S = 2 * a.P;
+  const long long first = (long long)w * R;
+  if (first >= a.T) return;
+  const int run_end = (int)min((long long)a.T, first + R);
+  if (a.mask)
+    for (long long i = first + lane * 128; i < run_end; i += 32 * 128) prefetch_l2(a.mask + i);
+  int s = seq_find_warp(a.cu, 0, S, (int)first);
+  grid_dependency_wait();  // coef
+  int end = -1;
+  float c = 0.f;
+  for (int p = (int)first; p < run_end; p += SEQ_PIECE) {
+    const int t = p + lane * SEQ_TOK;
+    if (t >= run_end) break;  // nothing below is collective
+    const uint32_t on = load_mask(a.mask, t, a.T, a.vec != 0);
+    float g[SEQ_TOK];
+#pragma unroll
+    for (int j = 0; j < SEQ_TOK; ++j) {
+      if (t + j >= end && t + j < a.T) {
+        s = seq_advance(a.cu, S, s, t + j);
+        end = s < S - 1 ? __ldg(a.cu + s + 1) : a.T;
+        c = __ldcg(a.coef + s);
+      }
+      g[j] = (on >> j) & 1u ? c : 0.f;
+    }
+    store_tok(a.grad, t, a.T, a.vec != 0, g);
+  }
+}
+
+// The pairs' mean by one warp, in a fixed order.
+__device__ __forceinline__ void pref_mean(const PrefArgs& a) {
+  const int lane = threadIdx.x & 31;
+  Sum2 v;
+#pragma unroll 8
+  for (int i = lane; i < a.P; i += 32) v.add(__ldcg(a.pair_loss + i));
+  v = warp_sum(v);
+  if (lane == 0) a.loss[0] = v.value() / (float)a.P;
 }
 
 __global__ void __launch_bounds__(SEQ_THREADS)
-    pref_grad_kernel(const uint8_t* __restrict__ mask, const int32_t* __restrict__ cu,
-                     const float* __restrict__ coef, int T, int S, int vec,
-                     float* __restrict__ grad) {
-  __shared__ int range[2];
-  const int t0 = blockIdx.x * SEQ_CHUNK;
-  const int t1 = min(T, t0 + SEQ_CHUNK);
-  const int t = t0 + threadIdx.x * SEQ_TOK;
-  const uint32_t on = load_mask8(mask, t, T, vec != 0);
-  int s_lo, s_hi;
-  block_range(cu, S, t0, t1, range, s_lo, s_hi);
-  if (t >= t1) return;
-  int s = seq_find(cu, s_lo, s_hi, t);
-  float c = __ldg(coef + s);
-  float g[SEQ_TOK];
-#pragma unroll
-  for (int j = 0; j < SEQ_TOK; ++j) {
-    bool moved = false;
-    while (s < s_hi && t + j >= __ldg(cu + s + 1)) {
-      ++s;
-      moved = true;
-    }
-    if (moved) c = __ldg(coef + s);
-    g[j] = (on >> j) & 1u ? c : 0.f;
+    pref_sums_kernel(const PrefArgs a, int warps, int* status) {
+  grid_dependents_go();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0;  // the next launch records errors
+  pref_sums(a, blockIdx.x * SEQ_WARPS + (threadIdx.x >> 5), run_length(a.T, warps));
+}
+
+__global__ void __launch_bounds__(SEQ_THREADS)
+    pref_pairs_kernel(const PrefArgs a, int warps, int* status) {
+  const int i = blockIdx.x * SEQ_WARPS + (threadIdx.x >> 5);
+  grid_dependents_go();
+  grid_dependency_wait();
+  if (i < a.P) pref_pair(a, i, run_length(a.T, warps), status);
+}
+
+__global__ void __launch_bounds__(SEQ_THREADS) pref_grad_kernel(const PrefArgs a, int warps) {
+  if (a.grad)
+    pref_grads(a, blockIdx.x * SEQ_WARPS + (threadIdx.x >> 5), run_length(a.T, warps));
+  if (blockIdx.x == 0 && threadIdx.x < 32) {
+    grid_dependency_wait();
+    pref_mean(a);
   }
-  store_f8(grad, t, T, vec != 0, g);
+}
+
+// The three parts in one block, for batches that one block holds.
+__global__ void __launch_bounds__(PREF_ONE_THREADS)
+    pref_one_block_kernel(const PrefArgs a, int* status) {
+  constexpr int WARPS = PREF_ONE_THREADS / 32;
+  const int w = threadIdx.x >> 5;
+  const int R = run_length(a.T, WARPS);
+  if (threadIdx.x == 0) *status = 0;
+  pref_sums(a, w, R);
+  __syncthreads();
+  for (int i = w; i < a.P; i += WARPS) pref_pair(a, i, R, status);
+  __syncthreads();
+  if (w == WARPS - 1) pref_mean(a);
+  if (a.grad) pref_grads(a, w, R);
 }
 
 }  // namespace
 
-int seq_blocks(int T) { return (T + SEQ_CHUNK - 1) / SEQ_CHUNK; }
+// Blocks of the walks: as many as are resident at once, and none without a
+// piece of tokens for each warp.
+int seq_blocks(int T, int num_sms) {
+  const long long pieces = ((long long)T + SEQ_PIECE - 1) / SEQ_PIECE;
+  return (int)std::max<long long>(
+      1, std::min<long long>((pieces + SEQ_WARPS - 1) / SEQ_WARPS, (long long)SEQ_RESIDENT * num_sms));
+}
+int seq_warps(int T, int num_sms) { return seq_blocks(T, num_sms) * SEQ_WARPS; }
 
-cudaError_t launch_policy_loss(const PolicyArgs& a, int* status, cudaStream_t stream) {
+cudaError_t launch_policy_loss(const PolicyArgs& a, int num_sms, int* status,
+                               cudaStream_t stream) {
   const bool per_seq = a.reduction == 1;
-  const dim3 grid((unsigned)seq_blocks(a.T)), block(SEQ_THREADS);
-  if (per_seq || (a.mask && !a.count_here)) {
-    const cudaError_t e =
-        launch_kernel("policy_count", policy_count_kernel, grid, block, 0, stream, a.mask, a.cu,
-                      a.T, a.S, a.vec, per_seq ? a.n_seq : nullptr, a.n_count, a.ticket + 1);
-    if (e != cudaSuccess) return e;
-  }
-  if (per_seq || a.adv_per_seq)
-    return launch_kernel("policy_loss", policy_loss_kernel<true>, grid, block, 0, stream, a,
-                         status);
-  return launch_kernel("policy_loss", policy_loss_kernel<false>, grid, block, 0, stream, a, status);
+  const dim3 block(SEQ_THREADS);
+  const dim3 grid(policy_one_block(a.T, a.reduction) ? 1u : (unsigned)seq_blocks(a.T, num_sms));
+  const auto kernel = per_seq || a.adv_per_seq ? policy_loss_kernel<true> : policy_loss_kernel<false>;
+  if (!per_seq && (!a.mask || a.count_here))
+    return launch_kernel("policy_loss", kernel, grid, block, 0, stream, a, status);
+  // What the loss kernel reads before its wait was complete before the count began.
+  const cudaError_t e =
+      launch_kernel("policy_count", policy_count_kernel, grid, block, 0, stream, a.mask, a.cu, a.T,
+                    a.S, a.vec, per_seq ? a.n_seq : nullptr, a.n_count);
+  if (e != cudaSuccess) return e;
+  return launch_kernel_early("policy_loss", kernel, grid, block, stream, a, status);
 }
 
-cudaError_t launch_pref_loss(const PrefArgs& a, int* status, cudaStream_t stream) {
-  const dim3 grid((unsigned)seq_blocks(a.T)), block(SEQ_THREADS);
-  cudaError_t e;
-  if (a.T > 0) {
-    e = launch_kernel("pref_sums", pref_sums_kernel, grid, block, 0, stream, a.logp, a.ref_logp,
-                      a.mask, a.cu, a.T, 2 * a.P, a.vec, a.slot_sum, a.slot_n, status);
-    if (e != cudaSuccess) return e;
-  }
-  const int warps = SEQ_THREADS / 32;
-  e = launch_kernel("pref_pairs", pref_pairs_kernel, dim3((unsigned)((a.P + warps - 1) / warps)),
-                    block, 0, stream, a);
-  if (e != cudaSuccess || !a.grad || a.T == 0) return e;
-  return launch_kernel("pref_grad", pref_grad_kernel, grid, block, 0, stream, a.mask, a.cu, a.coef,
-                       a.T, 2 * a.P, a.vec, a.grad);
+cudaError_t launch_pref_loss(const PrefArgs& a, int num_sms, int* status, cudaStream_t stream) {
+  if (pref_one_block(a.T, a.P))
+    return launch_kernel("pref_one_block", pref_one_block_kernel, dim3(1), dim3(PREF_ONE_THREADS),
+                         0, stream, a, status);
+  const int blocks = seq_blocks(a.T, num_sms), warps = blocks * SEQ_WARPS;
+  const dim3 grid((unsigned)blocks), block(SEQ_THREADS);
+  cudaError_t e =
+      launch_kernel("pref_sums", pref_sums_kernel, grid, block, 0, stream, a, warps, status);
+  if (e != cudaSuccess) return e;
+  e = launch_kernel_early("pref_pairs", pref_pairs_kernel,
+                          dim3((unsigned)((a.P + SEQ_WARPS - 1) / SEQ_WARPS)), block, stream, a,
+                          warps, status);
+  if (e != cudaSuccess) return e;
+  return launch_kernel_early("pref_grad", pref_grad_kernel, a.grad ? grid : dim3(1), block, stream,
+                             a, warps);
 }
 
 }  // namespace kdkl

@@ -501,6 +501,35 @@ def kd_lmhead_topk(H, W, K, *, topk_idx=None, topk_logit=None, workspace=None, s
     return topk_idx, topk_logit
 
 
+def _addr(t, name, dtype, shape, dev):
+    """Address of an optional tensor argument after the checks of _check and
+    same_device, in one expression when all is well: the calls below are short
+    enough on the GPU for the host's part to count."""
+    if t is None:
+        return None
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda
+            and t.device == dev and t.is_contiguous()):
+        _check(t, name, dtype, shape)
+        same_device(dev, **{name: t})
+    return t.data_ptr()
+
+
+def _launch(fn_name, dev, stream, *args):
+    """_call for addresses that are plain integers, without its context manager
+    when ``dev`` is the current device already."""
+    lib = _lib or load()
+    if stream is not None and stream.device != dev:
+        raise ValueError("stream is on %s, expected %s" % (stream.device, dev))
+    raw = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        rc = getattr(lib, fn_name)(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            rc = getattr(lib, fn_name)(*args, raw)
+    if rc != KD_OK:
+        raise KDKLError(rc, fn_name)
+
+
 def _new(shape, dtype, dev, stream):
     """An output or workspace made here for a call on ``stream``: allocated as
     that stream's own memory, so that it is not handed to another stream's
@@ -516,9 +545,16 @@ def _given_workspace(workspace, need, where, dev, stream):
         raise KDKLError(2, where)
     if workspace is None:
         return _new(need, torch.uint8, dev, stream)
-    _check(workspace, "workspace", torch.uint8, (workspace.numel(),))
-    same_device(dev, workspace=workspace)
+    _addr(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
     return workspace
+
+
+def _outcome(t, name, dtype, shape, dev, stream):
+    """An output: the caller's, checked, or a new one."""
+    if t is None:
+        return _new(shape, dtype, dev, stream)
+    _addr(t, name, dtype, shape, dev)
+    return t
 
 
 def kd_logprob_workspace_size(T, d, V, temperature=1.0, chunk=1024, which=0,
@@ -531,30 +567,25 @@ def kd_logprob_workspace_size(T, d, V, temperature=1.0, chunk=1024, which=0,
 def _logprob_args(H, W, ids):
     T, d = H.shape
     V = W.shape[0]
-    _check(H, "H", torch.bfloat16, (T, d))
-    _check(W, "W", torch.bfloat16, (V, d))
-    _check(ids, "ids", torch.int32, (T,))
-    same_device(H.device, W=W, ids=ids)
-    return T, d, V, H.device
+    dev = H.device
+    return T, d, V, dev, (_addr(H, "H", torch.bfloat16, (T, d), dev),
+                          _addr(W, "W", torch.bfloat16, (V, d), dev),
+                          _addr(ids, "ids", torch.int32, (T,), dev))
 
 
 def kd_logprob_forward(H, W, ids, mask=None, *, temperature=1.0, logp=None, lse=None,
                        workspace=None, stream=None):
     """Log-probability of ids[t] under softmax(H[t] . W^T / temperature), the logits
     never stored. Returns (logp [T] fp32, lse [T] fp32); masked tokens read 0."""
-    T, d, V, dev = _logprob_args(H, W, ids)
-    if mask is not None:
-        _check(mask, "mask", torch.uint8, (T,))
-        same_device(dev, mask=mask)
+    T, d, V, dev, operands = _logprob_args(H, W, ids)
+    counted = _addr(mask, "mask", torch.uint8, (T,), dev)
     p = kd_logprob_problem(T, d, V, float(temperature), 0, 1)
     workspace = _given_workspace(workspace, load().kd_logprob_workspace_size(ctypes.byref(p), 0),
                                  "kd_logprob_workspace_size", dev, stream)
-    logp = _out(logp, "logp", torch.float32, (T,), dev)
-    lse = _out(lse, "lse", torch.float32, (T,), dev)
-    logp = _new(T, torch.float32, dev, stream) if logp is None else logp
-    lse = _new(T, torch.float32, dev, stream) if lse is None else lse
-    _call("kd_logprob_forward", dev, stream, ctypes.byref(p), _ptr(H), _ptr(W), _ptr(ids),
-          _ptr(mask), _ptr(logp), _ptr(lse), _ptr(workspace), workspace.numel())
+    logp = _outcome(logp, "logp", torch.float32, (T,), dev, stream)
+    lse = _outcome(lse, "lse", torch.float32, (T,), dev, stream)
+    _launch("kd_logprob_forward", dev, stream, ctypes.byref(p), *operands, counted,
+            logp.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel())
     return logp, lse
 
 
@@ -564,16 +595,13 @@ def kd_logprob_backward(H, W, ids, lse, grad_logp, *, temperature=1.0, chunk=102
     """Gradients of sum_t grad_logp[t] * logp[t]. Returns (dH [T,d] bf16, dW [V,d] in
     ``dW_dtype``: fp32, which may be added to, or bf16). Tokens whose gradient is
     zero are skipped."""
-    T, d, V, dev = _logprob_args(H, W, ids)
-    _check(lse, "lse", torch.float32, (T,))
-    _check(grad_logp, "grad_logp", torch.float32, (T,))
-    same_device(dev, lse=lse, grad_logp=grad_logp)
+    T, d, V, dev, operands = _logprob_args(H, W, ids)
+    given = (_addr(lse, "lse", torch.float32, (T,), dev),
+             _addr(grad_logp, "grad_logp", torch.float32, (T,), dev))
     if dW is not None:
         dW_dtype = dW.dtype
     if dW_dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("dW must be torch.float32 or torch.bfloat16, got %s" % dW_dtype)
-    dH = _out(dH, "dH", torch.bfloat16, (T, d), dev)
-    dW = _out(dW, "dW", dW_dtype, (V, d), dev)
     if accumulate_dW and dW is None:
         raise ValueError("accumulate_dW needs an existing dW")
     if accumulate_dW and dW_dtype == torch.bfloat16:
@@ -582,11 +610,10 @@ def kd_logprob_backward(H, W, ids, lse, grad_logp, *, temperature=1.0, chunk=102
                            int(chunk))
     workspace = _given_workspace(workspace, load().kd_logprob_workspace_size(ctypes.byref(p), 1),
                                  "kd_logprob_workspace_size", dev, stream)
-    dH = _new((T, d), torch.bfloat16, dev, stream) if dH is None else dH
-    dW = _new((V, d), dW_dtype, dev, stream) if dW is None else dW
-    _call("kd_logprob_backward", dev, stream, ctypes.byref(p), _ptr(H), _ptr(W), _ptr(ids),
-          _ptr(lse), _ptr(grad_logp), _ptr(dH), _ptr(dW), 1 if accumulate_dW else 0,
-          _ptr(workspace), workspace.numel())
+    dH = _outcome(dH, "dH", torch.bfloat16, (T, d), dev, stream)
+    dW = _outcome(dW, "dW", dW_dtype, (V, d), dev, stream)
+    _launch("kd_logprob_backward", dev, stream, ctypes.byref(p), *operands, *given, dH.data_ptr(),
+            dW.data_ptr(), 1 if accumulate_dW else 0, workspace.data_ptr(), workspace.numel())
     return dH, dW
 
 
@@ -604,37 +631,27 @@ def kd_policy_loss(logp, old_logp, ref_logp, advantages, mask=None, cu_seqlens=N
     grad_logp [T] = grad_loss * dloss/dlogp or None)."""
     T = logp.numel()
     dev = logp.device
-    _check(logp, "logp", torch.float32, (T,))
-    for name, t in (("old_logp", old_logp), ("ref_logp", ref_logp)):
-        if t is not None:
-            _check(t, name, torch.float32, (T,))
-    if mask is not None:
-        _check(mask, "mask", torch.uint8, (T,))
-    S = 0
-    if cu_seqlens is not None:
-        S = max(0, cu_seqlens.numel() - 1)
-        _check(cu_seqlens, "cu_seqlens", torch.int32, (S + 1,))
+    f32, flat = torch.float32, (T,)
+    S = 0 if cu_seqlens is None else max(0, cu_seqlens.numel() - 1)
     per_sequence = cu_seqlens is not None and advantages.numel() == S and S != T
-    _check(advantages, "advantages", torch.float32, (S if per_sequence else T,))
-    same_device(dev, old_logp=old_logp, ref_logp=ref_logp, advantages=advantages, mask=mask,
-                cu_seqlens=cu_seqlens)
+    given = (_addr(logp, "logp", f32, flat, dev), _addr(old_logp, "old_logp", f32, flat, dev),
+             _addr(ref_logp, "ref_logp", f32, flat, dev),
+             _addr(advantages, "advantages", f32, (S if per_sequence else T,), dev),
+             _addr(mask, "mask", torch.uint8, flat, dev),
+             _addr(cu_seqlens, "cu_seqlens", torch.int32, (S + 1,), dev))
     if reduction not in KD_REDUCTIONS:
         raise ValueError("reduction must be one of %s, got %r" % (sorted(KD_REDUCTIONS), reduction))
     p = kd_policy_problem(T, S, clip_low, clip_high, dual_clip, kl_coef if ref_logp is not None
                           else 0.0, norm, KD_REDUCTIONS[reduction], 1 if per_sequence else 0)
     need = load().kd_policy_workspace_size(ctypes.byref(p))
-    workspace = _given_workspace(workspace, need, "kd_policy_workspace_size", dev, stream) \
-        if need else _new(256, torch.uint8, dev, stream)  # the call names the error
-    loss = _out(loss, "loss", torch.float32, (1,), dev)
-    stats = _out(stats, "stats", torch.float32, (3,), dev)
-    grad_logp = _out(grad_logp, "grad_logp", torch.float32, (T,), dev)
-    loss = _new(1, torch.float32, dev, stream) if loss is None else loss
-    stats = _new(3, torch.float32, dev, stream) if stats is None else stats
-    if want_grad and grad_logp is None:
-        grad_logp = _new(T, torch.float32, dev, stream)
-    _call("kd_policy_loss", dev, stream, ctypes.byref(p), _ptr(logp), _ptr(old_logp),
-          _ptr(ref_logp), _ptr(advantages), _ptr(mask), _ptr(cu_seqlens), float(grad_loss),
-          _ptr(loss), _ptr(stats), _ptr(grad_logp), _ptr(workspace), workspace.numel())
+    workspace = _given_workspace(workspace, need or 256, "", dev, stream)  # 0: the call says why
+    loss = _outcome(loss, "loss", f32, (1,), dev, stream)
+    stats = _outcome(stats, "stats", f32, (3,), dev, stream)
+    if want_grad or grad_logp is not None:
+        grad_logp = _outcome(grad_logp, "grad_logp", f32, flat, dev, stream)
+    _launch("kd_policy_loss", dev, stream, ctypes.byref(p), *given, grad_loss, loss.data_ptr(),
+            stats.data_ptr(), None if grad_logp is None else grad_logp.data_ptr(),
+            workspace.data_ptr(), workspace.numel())
     return loss, stats, grad_logp
 
 
@@ -650,34 +667,27 @@ def kd_pref_loss(logp, ref_logp, cu_seqlens, mask=None, *, beta=0.1, kind="sigmo
     Returns (loss [1], rewards [P,2], grad_logp [T] = grad_loss * dloss/dlogp or None)."""
     T = logp.numel()
     dev = logp.device
-    _check(logp, "logp", torch.float32, (T,))
-    if ref_logp is not None:
-        _check(ref_logp, "ref_logp", torch.float32, (T,))
-    if mask is not None:
-        _check(mask, "mask", torch.uint8, (T,))
+    f32, flat = torch.float32, (T,)
     n = cu_seqlens.numel()
-    _check(cu_seqlens, "cu_seqlens", torch.int32, (n,))
+    given = (_addr(logp, "logp", f32, flat, dev), _addr(ref_logp, "ref_logp", f32, flat, dev),
+             _addr(mask, "mask", torch.uint8, flat, dev),
+             _addr(cu_seqlens, "cu_seqlens", torch.int32, (n,), dev))
     if n % 2 != 1:
         raise ValueError("cu_seqlens holds 2 P + 1 offsets, got %d" % n)
     P = n // 2
-    same_device(dev, ref_logp=ref_logp, mask=mask, cu_seqlens=cu_seqlens)
     if kind not in KD_PREF_KINDS:
         raise ValueError("kind must be one of %s, got %r" % (sorted(KD_PREF_KINDS), kind))
     p = kd_pref_problem(T, P, beta, label_smoothing, margin, KD_PREF_KINDS[kind],
                         1 if average else 0, 1 if halves else 0, 0)
     need = load().kd_pref_workspace_size(ctypes.byref(p))
-    workspace = _given_workspace(workspace, need, "kd_pref_workspace_size", dev, stream) \
-        if need else _new(256, torch.uint8, dev, stream)  # the call names the error
-    loss = _out(loss, "loss", torch.float32, (1,), dev)
-    rewards = _out(rewards, "rewards", torch.float32, (P, 2), dev)
-    grad_logp = _out(grad_logp, "grad_logp", torch.float32, (T,), dev)
-    loss = _new(1, torch.float32, dev, stream) if loss is None else loss
-    rewards = _new((P, 2), torch.float32, dev, stream) if rewards is None else rewards
-    if want_grad and grad_logp is None:
-        grad_logp = _new(T, torch.float32, dev, stream)
-    _call("kd_pref_loss", dev, stream, ctypes.byref(p), _ptr(logp), _ptr(ref_logp), _ptr(mask),
-          _ptr(cu_seqlens), float(grad_loss), _ptr(loss), _ptr(rewards), _ptr(grad_logp),
-          _ptr(workspace), workspace.numel())
+    workspace = _given_workspace(workspace, need or 256, "", dev, stream)  # 0: the call says why
+    loss = _outcome(loss, "loss", f32, (1,), dev, stream)
+    rewards = _outcome(rewards, "rewards", f32, (P, 2), dev, stream)
+    if want_grad or grad_logp is not None:
+        grad_logp = _outcome(grad_logp, "grad_logp", f32, flat, dev, stream)
+    _launch("kd_pref_loss", dev, stream, ctypes.byref(p), *given, grad_loss, loss.data_ptr(),
+            rewards.data_ptr(), None if grad_logp is None else grad_logp.data_ptr(),
+            workspace.data_ptr(), workspace.numel())
     return loss, rewards, grad_logp
 
 
@@ -754,14 +764,12 @@ def kd_adamw_step(tensors: KDAdamWTensors, *, lr, betas=(0.9, 0.999), eps=1e-8, 
     """One AdamW step, in place, on the tensors of kd_adamw_tensors. ``step`` counts from 1.
     The gradients are multiplied by ``grad_scale`` and, if given, by the device scalar
     ``grad_scale_dev`` ([1] fp32, a clip coefficient)."""
-    if grad_scale_dev is not None:
-        _check(grad_scale_dev, "grad_scale_dev", torch.float32, (1,))
-        same_device(tensors.device, grad_scale_dev=grad_scale_dev)
     o = kd_adamw_options(lr, betas[0], betas[1], eps, weight_decay, int(step),
-                         None if grad_scale_dev is None else grad_scale_dev.data_ptr(), grad_scale,
-                         tensors.param_bf16, tensors.grad_bf16, tensors.state_8bit)
+                         _addr(grad_scale_dev, "grad_scale_dev", torch.float32, (1,),
+                               tensors.device),
+                         grad_scale, tensors.param_bf16, tensors.grad_bf16, tensors.state_8bit)
     if tensors.n:
-        _call("kd_adamw_step", tensors.device, stream, tensors.table, tensors.n, ctypes.byref(o))
+        _launch("kd_adamw_step", tensors.device, stream, tensors.table, tensors.n, ctypes.byref(o))
 
 
 def kd_kl_check_status(workspace: torch.Tensor, stream=None) -> int:
