@@ -249,6 +249,7 @@ struct BwdPlan {
   // (none when the backward reads the forward's)
   size_t off_ctr;
   TeacherLayout tl;
+  int dH_parts;  // dH is summed in so many parts of a block's vocabulary
   size_t off_G, off_dH, total;
 };
 
@@ -343,11 +344,24 @@ double rmw_bytes(const BlockPlan& b, int64_t T, const kd_kl_problem& p) {
          ((double)(b.n_vblocks - 1) * (double)T + (double)(b.n_tblocks - 1) * (double)p.V);
 }
 
+// Parts of the dH product along a block's vocabulary: of few tokens it has fewer
+// 256 x 256 tiles than the 76 CTA pairs (12 for 640 tokens of d = 1000), each of
+// which then walks the whole vocabulary alone (32,003 columns: 208 us; in 10
+// parts 50). Enough parts for two units a pair, none shorter
+// than 8 steps of 64 columns.
+int dH_split(int64_t T, int64_t d, int64_t Vb) {
+  const int64_t tiles = ceil_div(T, 2 * BM) * ceil_div(d, 256);
+  if (tiles >= 76) return 1;
+  return (int)std::max<int64_t>(1, std::min(ceil_div(152, tiles), ceil_div(Vb, BK) / 8));
+}
+
 // own_teacher: the backward prepares the sorted teacher cache itself (sidx,
 // sp in its workspace); otherwise it reads the forward's.
 // whole_dW: every dW tile comes from one launch (all tokens per vocabulary
 // slab, however many there are), as a dW rounded to bf16 on its way out needs.
-BwdPlan plan_backward(const kd_kl_problem& p, bool own_teacher = true, bool whole_dW = false) {
+// split_dH: the dH products may be cut along the vocabulary (see dH_split).
+BwdPlan plan_backward(const kd_kl_problem& p, bool own_teacher = true, bool whole_dW = false,
+                      bool split_dH = false) {
   BwdPlan b{};
   const int64_t T = std::max<int64_t>(p.T, 1);
   const double budget = (double)p.chunk * (double)p.V;  // gradient-of-logits elements
@@ -368,7 +382,8 @@ BwdPlan plan_backward(const kd_kl_problem& p, bool own_teacher = true, bool whol
   b.tl = teacher_layout(o, p);
   if (own_teacher) o = b.tl.end;
   b.off_G = o; o = align256(o + (size_t)b.Tb_pad * b.Vb_pad * 2);
-  b.off_dH = o; o = align256(o + (size_t)p.T * p.d * 4);
+  b.dH_parts = split_dH ? dH_split(b.Tb, p.d, b.Vb) : 1;
+  b.off_dH = o; o = align256(o + (size_t)b.dH_parts * p.T * p.d * 4);
   b.total = o;
   return b;
 }
@@ -824,7 +839,9 @@ static kd_status backward_blocks(const kd_kl_problem& p, const BwdPlan& b, const
         // Units of 2 vocabulary tiles: nothing runs across tiles but each
         // row's cursor into its teacher ids, and short units keep the tail
         // of these short launches small.
-        const LogitPlan lp = plan_logit(rows, cols, d, tile_m, 2);
+        // (One tile for the few units of a short token-gradient launch.)
+        const bool few = j.row_grad && ceil_div(rows, tile_m) * ceil_div(cols, LOGIT_BN) <= 2 * procs;
+        const LogitPlan lp = plan_logit(rows, cols, d, tile_m, few ? 1 : 2);
         GemmShape sh{};
         sh.inject_stall = stall;
         sh.m_tiles = lp.m_tiles;
@@ -888,8 +905,10 @@ static kd_status backward_blocks(const kd_kl_problem& p, const BwdPlan& b, const
       sh_dh.n_tiles = dn_tiles;
       sh_dh.nsplit = dn_tiles;
       sh_dh.group_m = 1;  // m-major: an m-tile's output tiles run side by side
-      sh_dh.units = sh_dh.m_tiles * sh_dh.nsplit;
       sh_dh.k_blocks = (int)ceil_div(cols, BK);
+      // (a part of the last, shorter block may have no step: then there are fewer)
+      sh_dh.k_parts = std::min(b.dH_parts, sh_dh.k_blocks);
+      sh_dh.units = sh_dh.m_tiles * sh_dh.nsplit * std::max(1, sh_dh.k_parts);
       sh_dh.b_k0 = col0;
       sh_dh.narrow_last = narrow_last;
       if (compact) {
@@ -901,6 +920,7 @@ static kd_status backward_blocks(const kd_kl_problem& p, const BwdPlan& b, const
       EpiParams ep_dh{};
       ep_dh.out = dH_acc + (int64_t)row0 * d;
       ep_dh.ldo = d;
+      ep_dh.part_stride = p.T * p.d;
       ep_dh.out_rows = rows;
       ep_dh.out_cols = d;
       ep_dh.accumulate = vb > 0 ? 1 : 0;
@@ -961,7 +981,8 @@ static kd_status backward_blocks(const kd_kl_problem& p, const BwdPlan& b, const
           print_plan("dW (job 0)", pair, procs, sh_dw, grid);
           print_plan("dH (job 1)", pair, procs, sh_dh, grid);
         }
-        const bool dh_first = sh_dh.k_blocks > sh_dw.k_blocks;  // longer units first
+        // longer units first
+        const bool dh_first = sh_dh.k_blocks / std::max(1, sh_dh.k_parts) > sh_dw.k_blocks;
         KD_CUDA(launch_gemm_dw_dh(pair, dh_first, tmG_MN, tmH_MN, sh_dw, ep_dw, tmG_K, tmW_MN,
                                   sh_dh, ep_dh, status, grid, stream));
       }
@@ -1259,15 +1280,16 @@ static kd_status logprob_validate(const kd_logprob_problem* p, const void* H, co
   return validate_common(&q, H, W, ids, ids, workspace);
 }
 
-// Vocabulary tiles per unit of the forward: 8 as in the KL forward when the
-// tiles fill the processors many times over, fewer when they do not (one tile
-// of tokens against a vocabulary of 786 tiles is 98 units of 8 for 76 pairs,
-// two rounds of which the second is a third full). Eight tiles need 16 units
-// for each processor.
+// Vocabulary tiles per unit of the forward, u. With n tiles a processor, each
+// costing the epilogue e, a unit's row state s on top and on average half a
+// unit's wait at the end, the time is about n e + n s / u + u e / 2: least at
+// u = sqrt(2 n s / e). s is about 1.3 us (two dependent loads from L2), e 5.4.
+// 8 at most, as in the KL forward. Measured at d = 1000, V = 32,003: the forward
+// of 4096 tokens 215 us with u = 1 (n = 26).
 static int logprob_split_tiles(const kd_kl_problem& p, bool pair, int procs) {
-  const int64_t tiles = ceil_div(p.V, LOGIT_BN) *
-                        std::max<int64_t>(1, ceil_div(p.T, pair ? 2 * BM : BM));
-  return (int)std::max<int64_t>(1, std::min<int64_t>(8, tiles / (16 * (int64_t)procs)));
+  const double n = (double)ceil_div(p.V, LOGIT_BN) *
+                   (double)std::max<int64_t>(1, ceil_div(p.T, pair ? 2 * BM : BM)) / procs;
+  return (int)std::max(1.0, std::min(8.0, std::round(std::sqrt(0.48 * n))));
 }
 
 static FwdPlan plan_logprob(const kd_kl_problem& p, int num_sms, bool pair, int procs) {
@@ -1277,7 +1299,7 @@ static FwdPlan plan_logprob(const kd_kl_problem& p, int num_sms, bool pair, int 
 size_t kd_logprob_workspace_size(const kd_logprob_problem* prob, int which) {
   kd_kl_problem p;
   if (!logprob_problem(prob, &p)) return 0;
-  if (which == 1) return plan_backward(p, true, prob->dw_bf16 != 0).total;
+  if (which == 1) return plan_backward(p, true, prob->dw_bf16 != 0, true).total;
   if (which != 0) return 0;
   DeviceInfo di;
   const int sms = (device_info(&di) == KD_OK) ? di.num_sms : 160;
@@ -1318,11 +1340,10 @@ kd_status kd_logprob_forward(const kd_logprob_problem* prob, const uint16_t* H, 
   int* invmap = compact ? at<int>(workspace, f.tl.off_invmap) : nullptr;
   uint16_t* Hc = at<uint16_t>(workspace, f.tl.off_Hc);
   const int64_t T_pad = round_up(T, 2 * BM);
-  if (compact) {
-    KD_CUDA(launch_mask_scan(mask, T, rowmap, invmap, n_count, stream));
-    KD_CUDA(launch_gather_rows(H, d, rowmap, n_count, T_pad, 2 * BM, Hc, di.num_sms, stream));
-  }
-  KD_CUDA(launch_label_prep(ids, rowmap, n_count, T, V, sidx, sp, status, stream));
+  float* zdot = at<float>(workspace, f.off_ent);
+  if (compact) KD_CUDA(launch_mask_scan(mask, T, rowmap, invmap, n_count, stream));
+  KD_CUDA(launch_token_rows(H, W, d, ids, rowmap, n_count, T, V, 2 * BM, compact ? Hc : nullptr,
+                            sidx, sp, zdot, status, di.num_sms, stream));
   CUtensorMap tmH, tmW;
   if (!encode_bf16_2d(&tmH, compact ? Hc : H, d, compact ? T_pad : T, d, BK, BM) ||
       !encode_bf16_2d(&tmW, W, d, V, d, BK, pair ? LOGIT_BN / 2 : LOGIT_BN))
@@ -1354,8 +1375,8 @@ kd_status kd_logprob_forward(const kd_logprob_problem* prob, const uint16_t* H, 
   ep.pd = at<float>(workspace, f.off_pd);
   if (log_plan()) print_plan("logprob", pair, gemm_procs(di.num_sms, pair), sh, f.grid);
   KD_CUDA(launch_gemm(GEMM_FWD_LSE, LOGIT_BN, pair, tmH, tmW, sh, ep, status, f.grid, stream));
-  KD_CUDA(launch_logp_combine(ep.pm, ep.ps, ep.pd, f.nsplit, T, invmap, cl2, inv_tau, logp, lse,
-                              stream));
+  KD_CUDA(launch_logp_combine(ep.pm, ep.ps, ep.pd, f.nsplit, T, invmap, zdot, cl2, inv_tau,
+                              logp, lse, stream));
   return KD_OK;
 }
 
@@ -1375,7 +1396,7 @@ kd_status kd_logprob_backward(const kd_logprob_problem* prob, const uint16_t* H,
   DeviceInfo di;
   if ((st = device_info(&di)) != KD_OK) return st;
   if ((st = get_encoder()) != KD_OK) return st;
-  const BwdPlan b = plan_backward(p, true, bf16);
+  const BwdPlan b = plan_backward(p, true, bf16, true);
   if (workspace_bytes < b.total) return KD_ERR_WORKSPACE;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
   forget_forward(workspace);
@@ -1395,9 +1416,8 @@ kd_status kd_logprob_backward(const kd_logprob_problem* prob, const uint16_t* H,
   uint16_t* Hc = at<uint16_t>(workspace, b.tl.off_Hc);
   // Only the tokens with a gradient, as the other calls do with a mask.
   KD_CUDA(launch_grad_scan(grad_logp, T, rowmap, invmap, n_count, stream));
-  KD_CUDA(launch_gather_rows(H, d, rowmap, n_count, round_up(T, 2 * BM), 2 * BM, Hc, di.num_sms,
-                             stream));
-  KD_CUDA(launch_label_prep(ids, rowmap, n_count, T, V, sidx, sp, status, stream));
+  KD_CUDA(launch_token_rows(H, W, d, ids, rowmap, n_count, T, V, 2 * BM, Hc, sidx, sp, nullptr,
+                            status, di.num_sms, stream));
   BackwardBlocks bb{};
   bb.H = H;
   bb.W = W;
@@ -1416,7 +1436,7 @@ kd_status kd_logprob_backward(const kd_logprob_problem* prob, const uint16_t* H,
   bb.accumulate_dW = accumulate_dW;
   if ((st = backward_blocks(p, b, bb, workspace, di.num_sms, stream)) != KD_OK) return st;
   KD_CUDA(launch_f32_to_bf16(at<float>(workspace, b.off_dH), dH, (long long)p.T * p.d, d, invmap,
-                             di.num_sms, stream));
+                             di.num_sms, stream, b.dH_parts));
   return KD_OK;
 }
 

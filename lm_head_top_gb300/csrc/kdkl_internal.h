@@ -107,9 +107,9 @@ cudaError_t launch_lse_combine_mix(const float* pm, const float* ps, const float
 cudaError_t launch_loss_finalize(const double* block_sums, int nblocks, const int* n_count,
                                  float* loss, cudaStream_t stream);
 // out [T, d] bf16 <- in rows (invmap[t], or t when invmap is nullptr; zeros
-// for invmap[t] < 0); n = T * d.
+// for invmap[t] < 0); n = T * d; the sum of `parts` such arrays, n apart.
 cudaError_t launch_f32_to_bf16(const float* in, uint16_t* out, long long n, int d,
-                               const int* invmap, int num_sms, cudaStream_t stream);
+                               const int* invmap, int num_sms, cudaStream_t stream, int parts = 1);
 // merge of per-split top-K lists; shared memory = topk_merge_p2() * 8 bytes
 int topk_merge_p2(int nsplit, int K);
 cudaError_t launch_topk_merge(const float* unit_val, const int32_t* unit_id, const int* unit_cnt,
@@ -174,12 +174,15 @@ cudaError_t launch_gemm_dw_dh(bool pair, bool dh_first, const CUtensorMap& tmG_M
 // Compaction of the tokens whose gradient is not zero (NaN included).
 cudaError_t launch_grad_scan(const float* grad, int T, int* rowmap, int* invmap, int* n_count,
                              cudaStream_t stream);
-// Row r's id and weight 1, as a teacher row of one entry; checks the id.
-cudaError_t launch_label_prep(const int32_t* ids, const int* rowmap, const int* n_count, int T,
-                              int V, int32_t* sidx, float* sp, int* status, cudaStream_t stream);
+// Row r's id and weight 1 as a teacher row of one entry, its row of H in Hc (or
+// null) and its own logit before scaling in zdot (or null); checks the id.
+cudaError_t launch_token_rows(const uint16_t* H, const uint16_t* W, int d, const int32_t* ids,
+                              const int* rowmap, const int* n_count, int T, int V, int round,
+                              uint16_t* Hc, int32_t* sidx, float* sp, float* zdot, int* status,
+                              int num_sms, cudaStream_t stream);
 cudaError_t launch_logp_combine(const float* pm, const float* ps, const float* pd, int nsplit,
-                                int T, const int* invmap, float cl2, float inv_tau, float* logp,
-                                float* lse, cudaStream_t stream);
+                                int T, const int* invmap, const float* zdot, float cl2,
+                                float inv_tau, float* logp, float* lse, cudaStream_t stream);
 
 // kernels_policy.cu
 struct PolicyArgs {

@@ -406,9 +406,11 @@ __global__ void __launch_bounds__(1024)
 }
 
 // out row t = bf16(in row invmap[t]), or zeros when invmap[t] < 0; invmap
-// nullptr: row t. One block per row at a time, d4 = d / 4 float4 per row.
+// nullptr: row t. One block per row at a time, d4 = d / 4 float4 per row. With
+// more than one part (part_stride4 float4 apart) the row is their sum, in order.
 __global__ void f32_to_bf16_kernel(const float4* __restrict__ in, uint2* __restrict__ out, int T,
-                                   int d4, const int* __restrict__ invmap) {
+                                   int d4, const int* __restrict__ invmap, int parts,
+                                   long long part_stride4) {
   for (int t = blockIdx.x; t < T; t += gridDim.x) {
     const int r = invmap ? __ldg(invmap + t) : t;
     uint2* o = out + (long long)t * d4;
@@ -418,7 +420,15 @@ __global__ void f32_to_bf16_kernel(const float4* __restrict__ in, uint2* __restr
     }
     const float4* src = in + (long long)r * d4;
     for (int c = threadIdx.x; c < d4; c += blockDim.x) {
-      const float4 v = src[c];
+      float4 v = src[c];
+#pragma unroll 4
+      for (int k = 1; k < parts; ++k) {
+        const float4 p = src[k * part_stride4 + c];
+        v.x += p.x;
+        v.y += p.y;
+        v.z += p.z;
+        v.w += p.w;
+      }
       o[c] = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
     }
   }
@@ -427,9 +437,10 @@ __global__ void f32_to_bf16_kernel(const float4* __restrict__ in, uint2* __restr
 // Compaction of the counted tokens, one block: rowmap[r] = the r-th token
 // with mask != 0 (in order), invmap[t] = its r or -1, *n_count = N. The mask
 // is taken in tiles of 32 x 1024 tokens: warp w owns 32 consecutive 32-token
-// chunks of a tile, counts them with ballots (lane j keeps chunk j's count),
-// a block scan gives each chunk its first row, and a second pass writes the
-// maps. Loads and invmap stores are coalesced 32-token pieces.
+// chunks of a tile and takes their ballots, eight loads in flight (lane j keeps
+// chunk j's), a block scan gives each chunk its first row, and the maps are
+// written from the ballots. Loads and invmap stores are coalesced 32-token
+// pieces; chunks past the last token are passed over.
 // M: the mask's bytes, or the tokens' fp32 gradients (NaN counts).
 constexpr int SCAN_THREADS = 1024;
 template <typename M>
@@ -444,13 +455,17 @@ __global__ void __launch_bounds__(SCAN_THREADS)
   int base = 0;                                     // rows before this tile
   for (long long t0 = 0; t0 < T; t0 += TILE) {
     const long long w0 = t0 + (long long)warp * 32 * 32;  // this warp's first token
-    int my_count = 0;                                     // chunk `lane` of this warp
-    for (int j = 0; j < 32; ++j) {
+    // the warp's chunks that hold tokens
+    const int chunks = (int)max(0ll, min(32ll, (T - w0 + 31) / 32));
+    uint32_t mine = 0;  // chunk `lane`'s ballot
+#pragma unroll 8
+    for (int j = 0; j < chunks; ++j) {
       const long long t = w0 + (long long)j * 32 + lane;
       const bool on = t < T && mask[t] != (M)0;
-      const int c = __popc(__ballot_sync(0xffffffffu, on));
-      if (lane == j) my_count = c;
+      const uint32_t b = __ballot_sync(0xffffffffu, on);
+      if (lane == j) mine = b;
     }
+    const int my_count = __popc(mine);
     int incl = my_count;  // chunks of this warp, in order
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -472,10 +487,10 @@ __global__ void __launch_bounds__(SCAN_THREADS)
     }
     __syncthreads();
     const int chunk_first = base + warp_base[warp] + incl - my_count;  // chunk `lane`'s first row
-    for (int j = 0; j < 32; ++j) {
+    for (int j = 0; j < chunks; ++j) {
       const long long t = w0 + (long long)j * 32 + lane;
-      const bool on = t < T && mask[t] != (M)0;
-      const uint32_t b = __ballot_sync(0xffffffffu, on);
+      const uint32_t b = __shfl_sync(0xffffffffu, mine, j);
+      const bool on = (b >> lane) & 1u;
       const int first = __shfl_sync(0xffffffffu, chunk_first, j);
       if (t < T) {
         const int r = first + __popc(b & below);
@@ -489,30 +504,79 @@ __global__ void __launch_bounds__(SCAN_THREADS)
   if (threadIdx.x == 0) *n_count = base;
 }
 
-// Rows of one teacher entry each: the token's own id with weight 1, so that
-// the GEMM epilogues pick z at that id and subtract its one-hot.
-__global__ void label_prep_kernel(const int32_t* __restrict__ ids, const int* __restrict__ rowmap,
-                                  const int* __restrict__ n_count, int T, int V,
-                                  int32_t* __restrict__ sidx, float* __restrict__ sp,
-                                  int* __restrict__ status) {
-  const int r = blockIdx.x * blockDim.x + threadIdx.x;
-  if (r >= (rowmap ? min(*n_count, T) : T)) return;
-  const int id = ids[rowmap ? rowmap[r] : r];
-  if (id < 0 || id >= V) record_error(status, DEV_ERR_INDEX_RANGE);
-  sidx[r] = id;
-  sp[r] = 1.f;
+// A row per counted token, a warp each: the token's id with weight 1 as a
+// teacher row of one entry, so that the GEMM epilogues pick z at that id and
+// subtract its one-hot; with Hc, the token's row of H copied there (rows from N
+// to the end of N's last tile of `round` are zeroed); with zdot, the id's logit
+// before scaling, H row . W row in fp32 (a lane's products, then a tree).
+__global__ void __launch_bounds__(256)
+    token_rows_kernel(const uint4* __restrict__ H, const uint4* __restrict__ W, int row16,
+                      const int32_t* __restrict__ ids, const int* __restrict__ rowmap,
+                      const int* __restrict__ n_count, int T, int V, int round,
+                      uint4* __restrict__ Hc, int32_t* __restrict__ sidx, float* __restrict__ sp,
+                      float* __restrict__ zdot, int* __restrict__ status) {
+  const int lane = threadIdx.x & 31;
+  const int N = rowmap ? min(*n_count, T) : T;
+  const long long end = Hc ? ((long long)N + round - 1) / round * round : N;
+  const long long warps = (long long)gridDim.x * (blockDim.x >> 5);
+  for (long long r = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); r < end;
+       r += warps) {
+    uint4* o = Hc ? Hc + r * row16 : nullptr;
+    if (r >= N) {
+      for (int c = lane; c < row16; c += 32) o[c] = make_uint4(0u, 0u, 0u, 0u);
+      continue;
+    }
+    const int tok = rowmap ? __ldg(rowmap + r) : (int)r;
+    const int id = __ldg(ids + tok);
+    const bool known = id >= 0 && id < V;
+    if (lane == 0) {
+      if (!known) record_error(status, DEV_ERR_INDEX_RANGE);
+      sidx[r] = id;
+      sp[r] = 1.f;
+    }
+    const uint4* h = H + (long long)tok * row16;
+    const uint4* w = W + (long long)(known ? id : 0) * row16;
+    float dot = 0.f;
+#pragma unroll 4
+    for (int c = lane; c < row16; c += 32) {
+      const uint4 x = __ldg(h + c);
+      if (o) o[c] = x;
+      if (zdot) {
+        const uint4 y = __ldg(w + c);
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+        float part = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          part = fmaf(__uint_as_float(xs[k] << 16), __uint_as_float(ys[k] << 16), part);
+          part = fmaf(__uint_as_float(xs[k] & 0xffff0000u), __uint_as_float(ys[k] & 0xffff0000u),
+                      part);
+        }
+        dot += part;
+      }
+    }
+    if (zdot) {
+#pragma unroll
+      for (int k = 16; k > 0; k >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, k);
+      if (lane == 0) zdot[r] = dot;
+    }
+  }
 }
 
 // Per token, the vocabulary splits' partials (max, sum of exponentials, the
 // logit at the token's id) to lse and logp = (z - max)/tau - log(sum): the
-// maximum cancels before it is scaled. TOK tokens per block, 256 / TOK threads
-// on each one's splits, merged in a fixed order. invmap as in lse_combine.
+// maximum cancels before it is scaled. The tensor core's sum of d products loses
+// digits (1e-6 of a logit at d = 2880) that the token's own logit, often the
+// largest of its row, hands on to logp and lse in full; zdot has it in fp32 sums,
+// and its share of the sum of exponentials is corrected with it:
+// log(S + e^z' - e^z) = log S + log(1 + p (e^(z'-z) - 1)), p = e^z / S.
+// TOK tokens per block, 256 / TOK threads on each one's splits, merged in a
+// fixed order. invmap as in lse_combine.
 template <int TOK>
 __global__ void __launch_bounds__(COMBINE_THREADS)
     logp_combine_kernel(const float* __restrict__ pm, const float* __restrict__ ps,
                         const float* __restrict__ pd, int nsplit, int T,
-                        const int* __restrict__ invmap, float cl2, float inv_tau,
-                        float* __restrict__ logp, float* __restrict__ lse) {
+                        const int* __restrict__ invmap, const float* __restrict__ zdot, float cl2,
+                        float inv_tau, float* __restrict__ logp, float* __restrict__ lse) {
   constexpr int STRANDS = COMBINE_THREADS / TOK;
   const int i = threadIdx.x % TOK, w = threadIdx.x / TOK;
   const int t = blockIdx.x * TOK + i;
@@ -545,9 +609,17 @@ __global__ void __launch_bounds__(COMBINE_THREADS)
     }
   }
   if (w == 0 && t < T) {
-    const float top = part[0][0][i], rest = logf(part[1][0][i]);
-    lse[t] = r >= 0 ? fmaf(top, inv_tau, rest) : 0.f;
-    logp[t] = r >= 0 ? fmaf(part[2][0][i] - top, inv_tau, -rest) : 0.f;
+    float l = 0.f, lp = 0.f;
+    if (r >= 0) {
+      const float top = part[0][0][i], z = part[2][0][i], zd = zdot[r];
+      float rest = logf(part[1][0][i]);
+      const float p = expf(fmaf(z - top, inv_tau, -rest));
+      rest += log1pf(p * expm1f((zd - z) * inv_tau));
+      l = fmaf(top, inv_tau, rest);
+      lp = fmaf(zd - top, inv_tau, -rest);
+    }
+    lse[t] = l;
+    logp[t] = lp;
   }
 }
 
@@ -858,12 +930,12 @@ cudaError_t launch_gather_rows(const uint16_t* H, int d, const int* rowmap, cons
 }
 
 cudaError_t launch_f32_to_bf16(const float* in, uint16_t* out, long long n, int d,
-                               const int* invmap, int num_sms, cudaStream_t stream) {
+                               const int* invmap, int num_sms, cudaStream_t stream, int parts) {
   const int T = (int)(n / d);  // n = T * d, d a multiple of 8
   const int blocks = std::max(1, std::min(T, num_sms * 8));
   return launch_kernel("f32_to_bf16", f32_to_bf16_kernel, dim3((unsigned)blocks), dim3(256), 0,
                        stream, reinterpret_cast<const float4*>(in), reinterpret_cast<uint2*>(out),
-                       T, d / 4, invmap);
+                       T, d / 4, invmap, parts, n / 4);
 }
 
 cudaError_t launch_grad_scan(const float* grad, int T, int* rowmap, int* invmap, int* n_count,
@@ -872,23 +944,28 @@ cudaError_t launch_grad_scan(const float* grad, int T, int* rowmap, int* invmap,
                        grad, T, rowmap, invmap, n_count);
 }
 
-cudaError_t launch_label_prep(const int32_t* ids, const int* rowmap, const int* n_count, int T,
-                              int V, int32_t* sidx, float* sp, int* status, cudaStream_t stream) {
-  return launch_kernel("label_prep", label_prep_kernel, dim3((T + 255) / 256), dim3(256), 0, stream,
-                       ids, rowmap, n_count, T, V, sidx, sp, status);
+cudaError_t launch_token_rows(const uint16_t* H, const uint16_t* W, int d, const int32_t* ids,
+                              const int* rowmap, const int* n_count, int T, int V, int round,
+                              uint16_t* Hc, int32_t* sidx, float* sp, float* zdot, int* status,
+                              int num_sms, cudaStream_t stream) {
+  const int blocks = std::min((T + (Hc ? round : 0) + 7) / 8, num_sms * 8);
+  return launch_kernel("token_rows", token_rows_kernel, dim3((unsigned)blocks), dim3(256), 0,
+                       stream, reinterpret_cast<const uint4*>(H), reinterpret_cast<const uint4*>(W),
+                       d / 8, ids, rowmap, n_count, T, V, round, reinterpret_cast<uint4*>(Hc), sidx,
+                       sp, zdot, status);
 }
 
 cudaError_t launch_logp_combine(const float* pm, const float* ps, const float* pd, int nsplit,
-                                int T, const int* invmap, float cl2, float inv_tau, float* logp,
-                                float* lse, cudaStream_t stream) {
+                                int T, const int* invmap, const float* zdot, float cl2,
+                                float inv_tau, float* logp, float* lse, cudaStream_t stream) {
   // Few tokens: more threads on each one's splits, and more blocks.
   if (T <= 4096)
     return launch_kernel("logp_combine", logp_combine_kernel<4>, dim3((T + 3) / 4),
-                         dim3(COMBINE_THREADS), 0, stream, pm, ps, pd, nsplit, T, invmap, cl2,
-                         inv_tau, logp, lse);
+                         dim3(COMBINE_THREADS), 0, stream, pm, ps, pd, nsplit, T, invmap,
+                         zdot, cl2, inv_tau, logp, lse);
   return launch_kernel("logp_combine", logp_combine_kernel<32>, dim3((T + 31) / 32),
-                       dim3(COMBINE_THREADS), 0, stream, pm, ps, pd, nsplit, T, invmap, cl2,
-                       inv_tau, logp, lse);
+                       dim3(COMBINE_THREADS), 0, stream, pm, ps, pd, nsplit, T, invmap,
+                       zdot, cl2, inv_tau, logp, lse);
 }
 
 }  // namespace kdkl

@@ -45,6 +45,13 @@ constexpr uint32_t MN_ATOM_BYTES = BK * 128;
 // N tile of the logit GEMMs (vocabulary direction).
 constexpr int LOGIT_BN = 256;
 
+// Each epilogue warp's staging area: 32 rows of 128 bytes. A thread holds one
+// row of the accumulator, so a warp's direct 16-byte stores touch 32 lines each:
+// 128 line accesses for 64 columns of bf16, 4.3 us of the SM's store path per
+// 128 x 256 tile, more than a tile's MMAs below ~1,300 products deep. Staged,
+// the warp writes whole 128-byte row pieces: 32 line accesses.
+constexpr int EPI_WARP_BYTES = 32 * 128;
+
 // Shared-memory plan for an MMA tile of TILE_M x BN. With PAIR, two CTAs of a
 // cluster share one 256 x BN tile: each holds 128 rows of A and BN/2 rows of B
 // (so half the B bytes per CTA) and its own 128 x BN accumulator. As many
@@ -59,7 +66,10 @@ struct TileCfg {
   static constexpr int STAGES = (200 * 1024) / STAGE_BYTES > 8 ? 8 : (200 * 1024) / STAGE_BYTES;
   // full, empty, tmem full x2, tmem empty x2, drain, unit-slot full / empty
   static constexpr int NUM_BARS = 2 * STAGES + 5 + 2 * 4;
-  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 /*alignment slack*/ + 512;
+  static constexpr int BAR_BYTES = 512;  // barriers, the unit ring, flags
+  static_assert(NUM_BARS * 8 + 64 <= BAR_BYTES, "barrier region");
+  static constexpr int SMEM_BYTES =
+      STAGES * STAGE_BYTES + 1024 /*alignment slack*/ + BAR_BYTES + 4 * EPI_WARP_BYTES;
 };
 
 enum { EPI_LSE = 0, EPI_GRAD = 1, EPI_STORE = 2, EPI_TOPK = 3, EPI_LSE_MIX = 4, EPI_GRAD_MIX = 5 };
@@ -77,6 +87,11 @@ enum { EPI_LSE = 0, EPI_GRAD = 1, EPI_STORE = 2, EPI_TOPK = 3, EPI_LSE_MIX = 4, 
 struct GemmShape {
   int m_tiles, n_tiles, nsplit, group_m, units;
   int k_blocks;
+  // Above 1 (store epilogues): the K steps are cut into so many parts, each its
+  // own units (part 0's first) and its own output (EpiParams::part_stride apart),
+  // to be added up afterwards in part order: for outputs of fewer tiles than
+  // there are processors.
+  int k_parts;
   int a_m0, a_k0;  // A coordinate offsets (rows M / reduction K)
   int b_n0, b_k0;  // B coordinate offsets (rows N / reduction K)
   // Failure-detection test only: the producer issues nothing, so the MMA
@@ -105,6 +120,19 @@ struct GemmShape {
   // and each CTA copies half of its B rows: half the padded work and B bytes.
   int narrow_last;
 };
+
+// Takes unit u's K part off its number; the part, and its K steps [kb, ke).
+__device__ __forceinline__ int unit_k_part(const GemmShape& sh, int& u, int& kb, int& ke) {
+  kb = 0;
+  ke = sh.k_blocks;
+  if (sh.k_parts <= 1) return 0;
+  const int per = sh.m_tiles * sh.nsplit;
+  const int part = u / per;
+  u -= part * per;
+  kb = (int)((long long)part * sh.k_blocks / sh.k_parts);
+  ke = (int)((long long)(part + 1) * sh.k_blocks / sh.k_parts);
+  return part;
+}
 
 // n-tile range [nb, ne) of split s.
 __device__ __forceinline__ void split_range(const GemmShape& sh, int s, int& nb, int& ne) {
@@ -151,6 +179,7 @@ struct EpiParams {
   float* out;
   uint16_t* out16;  // bf16 output instead of `out` (stored, not accumulated), or null
   int64_t ldo;
+  int64_t part_stride;  // elements between the outputs of K parts
   int out_rows, out_cols;
   int accumulate;
   // EPI_LSE_MIX / EPI_GRAD_MIX: soft KL mixed with a hard-label cross-entropy
@@ -324,7 +353,7 @@ __device__ __forceinline__ int shrink_shape(GemmShape& sh) {
   const int a = max(0, min(*sh.dyn_rows - sh.dyn_base, sh.dyn_cap));
   if (sh.dyn_dim == 0) {
     sh.m_tiles = min(sh.m_tiles, (a + TILE_M - 1) / TILE_M);
-    sh.units = sh.m_tiles * sh.nsplit;
+    sh.units = sh.m_tiles * sh.nsplit * max(1, sh.k_parts);
     return a;
   }
   sh.k_blocks = min(sh.k_blocks, (a + BK - 1) / BK);
@@ -521,6 +550,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
         const bool j1 = job_of(u, js, uu, a_mn);
         const CUtensorMap* ta = j1 ? &tmA1 : &tmA;
         const CUtensorMap* tb = j1 ? &tmB1 : &tmB;
+        int kb0 = 0, kb1 = js->k_blocks;
+        if (EPI == EPI_STORE) unit_k_part(*js, uu, kb0, kb1);
         int m, s, nb, ne;
         unit_coords(*js, uu, m, s, nb, ne);
         const int a_row = js->a_m0 + m * TILE_M + (int)rank * BM;
@@ -529,7 +560,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
           const int b_rows = narrow ? B_ROWS / 2 : B_ROWS;  // B rows this CTA copies
           const int b_row = js->b_n0 + n * BN + (int)rank * b_rows;
           const uint32_t stage_bytes = (uint32_t)(A_STAGE_BYTES + b_rows * BK * 2);
-          for (int kb = 0; kb < js->k_blocks; ++kb) {
+          for (int kb = kb0; kb < kb1; ++kb) {
             if (!mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, status, limit)) {
               ok = false;
               break;
@@ -598,6 +629,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
         // the epilogue writes zeros without touching TMEM.
         if (js->k_blocks == 0) continue;
         const uint32_t idesc = j1 ? idesc1 : idesc0;
+        int kb0 = 0, kb1 = js->k_blocks;
+        if (EPI == EPI_STORE) unit_k_part(*js, uu, kb0, kb1);
         int m, s, nb, ne;
         unit_coords(*js, uu, m, s, nb, ne);
         for (int n = nb; ok && n < ne; ++n) {
@@ -615,7 +648,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
           }
           tc_fence_after();
           const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
-          for (int kb = 0; kb < js->k_blocks; ++kb) {
+          for (int kb = kb0; kb < kb1; ++kb) {
             if (!mbar_wait_bounded(full_bar(stage), phase, abort_flag, status, limit)) {
               ok = false;
               break;
@@ -630,9 +663,9 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
               const uint64_t bd = B_MN ? sdesc_sw128(b_base + k * 2048, MN_ATOM_BYTES, 1024)
                                        : sdesc_sw128(b_base + k * 32, 16, 1024);
               if (PAIR)
-                tc_mma_bf16_pair(d_tmem, ad, bd, idesc_n, (kb | k) != 0 ? 1u : 0u);
+                tc_mma_bf16_pair(d_tmem, ad, bd, idesc_n, (kb != kb0 || k != 0) ? 1u : 0u);
               else
-                tc_mma_bf16(d_tmem, ad, bd, idesc_n, (kb | k) != 0 ? 1u : 0u);
+                tc_mma_bf16(d_tmem, ad, bd, idesc_n, (kb != kb0 || k != 0) ? 1u : 0u);
             }
             if (PAIR)
               tc_commit_pair_multicast(empty_bar(stage), 0x3);
@@ -668,6 +701,51 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     uint32_t acc_phase = 0;
     bool ok = true;
     const uint32_t tempty_remote0 = PAIR ? mapa_shared(tempty_bar(0), 0) : 0u;
+    // Staging (see EPI_WARP_BYTES): 16-byte chunk c of row r lies at chunk
+    // c ^ (r & 7), so that neither the rows' writes nor the pieces' reads meet
+    // in a bank. One warp per scheduler does this alone, so every instruction
+    // counts: chunk addresses are one exclusive or, eight loads go out together,
+    // whole pieces are stored without a test.
+    const uint32_t stage0 =
+        smem_u32(smem) + STAGES * STAGE_BYTES + Cfg::BAR_BYTES + q * EPI_WARP_BYTES;
+    const uint32_t stage_row = stage0 + lane * 128 + ((lane & 7) << 4);  // chunk c: ^ (c << 4)
+    const uint32_t stage_even = stage0 + (lane >> 3) * 128 + (((lane & 7) ^ (lane >> 3)) << 4);
+    const uint32_t stage_odd =
+        stage0 + ((lane >> 3) + 4) * 128 + (((lane & 7) ^ ((lane >> 3) + 4)) << 4);
+    auto stage_bf16 = [&](const float (&x)[32], int c0) {  // 32 columns from chunk c0 on
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        st_shared_v4(stage_row ^ ((c0 + j) << 4),
+                     make_uint4(pack_bf16x2(x[8 * j + 0], x[8 * j + 1]),
+                                pack_bf16x2(x[8 * j + 2], x[8 * j + 3]),
+                                pack_bf16x2(x[8 * j + 4], x[8 * j + 5]),
+                                pack_bf16x2(x[8 * j + 6], x[8 * j + 7])));
+    };
+    // The staged rows to dst (row 0's first byte, ld_bytes apart), 8 lanes a row:
+    // `rows` of them, `chunks` chunks of each; added to fp32 there, or stored.
+    auto flush = [&](void* dst, int64_t ld_bytes, int rows, int chunks, bool add) {
+      __syncwarp();
+      uint4 w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        w[i] = ld_shared_v4((i & 1 ? stage_odd : stage_even) + (i >> 1) * 1024);
+      char* p = static_cast<char*>(dst) + (lane >> 3) * ld_bytes + (lane & 7) * 16;
+      const bool whole = rows >= 32 && chunks >= 8;
+      const bool mine = (lane & 7) < chunks;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (whole || (mine && 4 * i + (lane >> 3) < rows)) {
+          if (add)
+            red_add_f32x4(reinterpret_cast<float*>(p),
+                          make_float4(__uint_as_float(w[i].x), __uint_as_float(w[i].y),
+                                      __uint_as_float(w[i].z), __uint_as_float(w[i].w)));
+          else
+            *reinterpret_cast<uint4*>(p) = w[i];
+        }
+        p += 4 * ld_bytes;
+      }
+      __syncwarp();
+    };
     // EPI_TOPK: each (CTA, row) has two list banks. When a unit ends, the warp
     // switches bank and finishes the old unit's rows later (compaction to K
     // and write-out, one row at a time), in the waits for the next unit's
@@ -725,6 +803,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
       const bool j1 = job_of(u, js, uu, a_mn_unused);
       const EpiParams& eo = j1 ? ep1 : ep;  // the unit's output (store epilogues)
       const bool no_k = js->k_blocks == 0;  // zeros, no TMEM (see the MMA role)
+      int k_part = 0, kb_unused, ke_unused;
+      if (EPI == EPI_STORE) k_part = unit_k_part(*js, uu, kb_unused, ke_unused);
       int m, s, nb, ne;
       unit_coords(*js, uu, m, s, nb, ne);
       const int r = m * TILE_M + (int)rank * BM + r_in_tile;  // row within this launch
@@ -919,20 +999,16 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                 cur_id = cursor < ep.K ? __ldg(id_row + cursor) : 0x7fffffff;
               }
               if (MIX) scale = row_live ? 1.f : 0.f;  // weights already applied
-              if (!row_live) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) g[j] = 0.f;
-              }
-              uint4* dst = reinterpret_cast<uint4*>(ep.G + (long long)r * ep.ldg + cl);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                uint4 w;
-                w.x = pack_bf16x2(g[8 * j + 0] * scale, g[8 * j + 1] * scale);
-                w.y = pack_bf16x2(g[8 * j + 2] * scale, g[8 * j + 3] * scale);
-                w.z = pack_bf16x2(g[8 * j + 4] * scale, g[8 * j + 5] * scale);
-                w.w = pack_bf16x2(g[8 * j + 6] * scale, g[8 * j + 7] * scale);
-                dst[j] = w;
-              }
+              for (int j = 0; j < 32; ++j) g[j] = row_live ? g[j] * scale : 0.f;
+            }
+            // two pieces make a 128-byte row of the buffer (whose rows are whole
+            // 256-column tiles); the last piece of the columns may be alone
+            stage_bf16(g, 4 * (c & 1));
+            if ((c & 1) || cl + 32 >= ep.cols) {
+              const int r0 = r - lane;
+              flush(ep.G + (long long)r0 * ep.ldg + (cl - 32 * (c & 1)), 2 * ep.ldg, ep.rows - r0,
+                    (c & 1) ? 8 : 4, false);
             }
           } else if (EPI == EPI_TOPK) {
             const int vid0 = ep.col0 + cl;
@@ -945,36 +1021,26 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
               }
             }
           } else {  // EPI_STORE
-            if (r < eo.out_rows && eo.out16) {
-              uint4* dst = reinterpret_cast<uint4*>(eo.out16 + (long long)r * eo.ldo + cl);
-              const int nvalid = min(32, eo.out_cols - cl);  // multiple of 8
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                if (8 * j < nvalid) {
-                  uint4 w;
-                  w.x = pack_bf16x2(v[8 * j + 0], v[8 * j + 1]);
-                  w.y = pack_bf16x2(v[8 * j + 2], v[8 * j + 3]);
-                  w.z = pack_bf16x2(v[8 * j + 4], v[8 * j + 5]);
-                  w.w = pack_bf16x2(v[8 * j + 6], v[8 * j + 7]);
-                  dst[j] = w;
-                }
+            const int r0 = r - lane;
+            if (eo.out16) {
+              stage_bf16(v, 4 * (c & 1));
+              if ((c & 1) || cl + 32 >= eo.out_cols) {
+                const int cb = cl - 32 * (c & 1);
+                flush(eo.out16 + (long long)r0 * eo.ldo + cb, 2 * eo.ldo, eo.out_rows - r0,
+                      min((c & 1) ? 8 : 4, (eo.out_cols - cb) >> 3), false);
               }
-            } else if (r < eo.out_rows) {
-              float* dst = eo.out + (long long)r * eo.ldo + cl;
-              const int nvalid = min(32, eo.out_cols - cl);  // multiple of 4
+            } else {
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                if (4 * j < nvalid) {
-                  const float4 o = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-                  // Accumulate with a vector reduction: every element gets
-                  // exactly one add per launch and launches are stream-ordered,
-                  // so the sum order is fixed (deterministic).
-                  if (eo.accumulate)
-                    red_add_f32x4(dst + 4 * j, o);
-                  else
-                    *reinterpret_cast<float4*>(dst + 4 * j) = o;
-                }
-              }
+              for (int j = 0; j < 8; ++j)
+                st_shared_v4(stage_row ^ (j << 4),
+                             make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
+                                        __float_as_uint(v[4 * j + 2]),
+                                        __float_as_uint(v[4 * j + 3])));
+              // Accumulate with a vector reduction: every element gets exactly
+              // one add per launch and launches are stream-ordered, so the sum
+              // order is fixed (deterministic).
+              flush(eo.out + k_part * eo.part_stride + (long long)r0 * eo.ldo + cl, 4 * eo.ldo,
+                    eo.out_rows - r0, (eo.out_cols - cl) >> 2, eo.accumulate != 0);
             }
           }
         }

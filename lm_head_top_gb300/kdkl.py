@@ -557,7 +557,7 @@ def _outcome(t, name, dtype, shape, dev, stream):
     return t
 
 
-def kd_logprob_workspace_size(T, d, V, temperature=1.0, chunk=1024, which=0,
+def kd_logprob_workspace_size(T, d, V, temperature=1.0, chunk=4096, which=0,
                               dW_dtype=torch.float32) -> int:
     p = kd_logprob_problem(int(T), int(d), int(V), float(temperature),
                            1 if dW_dtype == torch.bfloat16 else 0, int(chunk))
@@ -589,7 +589,7 @@ def kd_logprob_forward(H, W, ids, mask=None, *, temperature=1.0, logp=None, lse=
     return logp, lse
 
 
-def kd_logprob_backward(H, W, ids, lse, grad_logp, *, temperature=1.0, chunk=1024, dH=None,
+def kd_logprob_backward(H, W, ids, lse, grad_logp, *, temperature=1.0, chunk=4096, dH=None,
                         dW=None, dW_dtype=torch.float32, accumulate_dW=False, workspace=None,
                         stream=None):
     """Gradients of sum_t grad_logp[t] * logp[t]. Returns (dH [T,d] bf16, dW [V,d] in
