@@ -236,11 +236,13 @@ struct AdamTensor {
 };
 struct AdamScalars {
   float b1, one_b1, b2, one_b2, inv_root_bc2, eps, step, keep, grad_scale;
+  int passes;  // of a thread block
   const float* grad_scale_dev;
 };
 constexpr int ADAMW_SHORT_LIST = 32;
 constexpr int ADAMW_LIST = 384;  // 30 KB of the 32,764 bytes a kernel's parameters may take
-int adamw_blocks(long long n);
+int adamw_passes(long long elements, bool state8, int num_sms);
+int adamw_blocks(long long n, int passes);
 cudaError_t launch_adamw(const AdamTensor* t, int n, int blocks, bool param_bf16, bool grad_bf16,
                          bool state8, const AdamScalars& s, cudaStream_t stream);
 

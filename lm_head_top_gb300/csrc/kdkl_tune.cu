@@ -235,10 +235,12 @@ kd_status kd_adamw_step(const kd_adamw_tensor* tensors, int32_t n_tensors,
   if (!aligned_to(o.grad_scale_dev, 4)) return KD_ERR_ALIGNMENT;
   const bool s8 = o.state_8bit != 0;
   const size_t pa = o.param_bf16 ? 2 : 4, ga = o.grad_bf16 ? 2 : 4, sa = s8 ? 1 : 4;
+  long long elements = 0;
   for (int i = 0; i < n_tensors; ++i) {
     const kd_adamw_tensor& t = tensors[i];
-    if (t.n < 0 || t.n >= (1ll << 40)) return KD_ERR_SHAPE;
+    if (t.n < 0 || t.n >= (1ll << 40)) return KD_ERR_SHAPE;  // 2^31 blocks of a pass at most
     if (t.n == 0) continue;
+    elements += t.n;
     if (!t.param || !t.grad || !t.exp_avg || !t.exp_avg_sq || (s8 && (!t.m_scale || !t.v_scale)))
       return KD_ERR_INVALID_ARG;
     if (!aligned_to(t.param, pa) || !aligned_to(t.grad, ga) || !aligned_to(t.exp_avg, sa) ||
@@ -260,6 +262,7 @@ kd_status kd_adamw_step(const kd_adamw_tensor* tensors, int32_t n_tensors,
   s.keep = (float)(1.0 - o.lr * o.weight_decay);
   s.grad_scale = o.grad_scale;
   s.grad_scale_dev = o.grad_scale_dev;
+  s.passes = adamw_passes(elements, s8, sms);
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
   AdamTensor list[ADAMW_LIST];
   int n = 0;
@@ -275,7 +278,7 @@ kd_status kd_adamw_step(const kd_adamw_tensor* tensors, int32_t n_tensors,
   for (int i = 0; i < n_tensors; ++i) {
     const kd_adamw_tensor& t = tensors[i];
     if (t.n == 0) continue;
-    const int64_t nb = adamw_blocks(t.n);
+    const int64_t nb = adamw_blocks(t.n, s.passes);
     if ((n == ADAMW_LIST || blocks + nb >= (1ll << 31) - 1) && !flush()) return KD_ERR_CUDA;
     AdamTensor& x = list[n++];
     x = AdamTensor{};

@@ -180,6 +180,12 @@ def test_many_blocks_and_scales(kdkl):
         _run(kdkl, [1 << 20, 3, (1 << 18) + 77], state8, grad_scale=0.25, eps=1e-6, step=1000)
 
 
+@pytest.mark.parametrize("n", [7_000_003, 13_000_300])
+def test_8bit_blocks_of_several_passes(kdkl, n):
+    """Enough elements for thread blocks that make 2 and 4 passes."""
+    _run(kdkl, [n, 5, 4097], True, g16=True)
+
+
 def test_device_scale(kdkl):
     n = 1000
     out = []
