@@ -794,6 +794,8 @@ static kd_status backward_blocks(const kd_kl_problem& p, const BwdPlan& b, const
   int launch_no = 0;  // index of the next GEMM launch's counter
   auto next_counter = [&]() { return counters ? counters + launch_no++ : nullptr; };
   const bool mix = j.opts != nullptr;
+  // Token gradients come in short calls too: their launches start early.
+  const bool early = j.row_grad != nullptr;
   const int T = (int)p.T, K = p.K, V = (int)p.V, d = (int)p.d;
   const float inv_tau = 1.0f / p.temperature;
   const float cl2 = 1.4426950408889634f * inv_tau;
@@ -888,7 +890,7 @@ static kd_status backward_blocks(const kd_kl_problem& p, const BwdPlan& b, const
         const int grid = cta_per_proc * (int)std::min<int64_t>(sh.units, procs);
         if (log_plan() && vb == 0 && tb == 0) print_plan("bwd_grad", pair, procs, sh, grid);
         KD_CUDA(launch_gemm(mix ? GEMM_BWD_GRAD_MIX : GEMM_BWD_GRAD, LOGIT_BN, pair, tmH_K, tmW_K,
-                            sh, ep, status, grid, stream));
+                            sh, ep, status, grid, stream, early));
       }
       // 2) dH[rows] (+)= G . W[cols] and 3) dW[cols] (+)= G^T . H[rows]: two
       // launches, or for small blocks one whose units run the job with the
@@ -966,12 +968,12 @@ static kd_status backward_blocks(const kd_kl_problem& p, const BwdPlan& b, const
         int grid = cta_per_proc * (int)std::min<int64_t>(sh_dh.units, procs);
         if (log_plan() && vb == 0 && tb == 0) print_plan("dH", pair, procs, sh_dh, grid);
         KD_CUDA(launch_gemm(GEMM_DH, out_bn, pair, tmG_K, tmW_MN, sh_dh, ep_dh, status, grid,
-                            stream));
+                            stream, early));
         sh_dw.counter = next_counter();
         grid = cta_per_proc * (int)std::min<int64_t>(sh_dw.units, procs);
         if (log_plan() && vb == 0 && tb == 0) print_plan("dW", pair, procs, sh_dw, grid);
         KD_CUDA(launch_gemm(GEMM_DW, out_bn, pair, tmG_MN, tmH_MN, sh_dw, ep_dw, status, grid,
-                            stream));
+                            stream, early));
       } else {
         // the launch's one counter, read from job 0's shape
         sh_dw.counter = sh_dh.counter = next_counter();
@@ -984,7 +986,7 @@ static kd_status backward_blocks(const kd_kl_problem& p, const BwdPlan& b, const
         // longer units first
         const bool dh_first = sh_dh.k_blocks / std::max(1, sh_dh.k_parts) > sh_dw.k_blocks;
         KD_CUDA(launch_gemm_dw_dh(pair, dh_first, tmG_MN, tmH_MN, sh_dw, ep_dw, tmG_K, tmW_MN,
-                                  sh_dh, ep_dh, status, grid, stream));
+                                  sh_dh, ep_dh, status, grid, stream, early));
       }
     }
   }
@@ -1374,7 +1376,8 @@ kd_status kd_logprob_forward(const kd_logprob_problem* prob, const uint16_t* H, 
   ep.ps = at<float>(workspace, f.off_ps);
   ep.pd = at<float>(workspace, f.off_pd);
   if (log_plan()) print_plan("logprob", pair, gemm_procs(di.num_sms, pair), sh, f.grid);
-  KD_CUDA(launch_gemm(GEMM_FWD_LSE, LOGIT_BN, pair, tmH, tmW, sh, ep, status, f.grid, stream));
+  KD_CUDA(launch_gemm(GEMM_FWD_LSE, LOGIT_BN, pair, tmH, tmW, sh, ep, status, f.grid, stream,
+                      true));
   KD_CUDA(launch_logp_combine(ep.pm, ep.ps, ep.pd, f.nsplit, T, invmap, zdot, cl2, inv_tau,
                               logp, lse, stream));
   return KD_OK;
@@ -1436,7 +1439,7 @@ kd_status kd_logprob_backward(const kd_logprob_problem* prob, const uint16_t* H,
   bb.accumulate_dW = accumulate_dW;
   if ((st = backward_blocks(p, b, bb, workspace, di.num_sms, stream)) != KD_OK) return st;
   KD_CUDA(launch_f32_to_bf16(at<float>(workspace, b.off_dH), dH, (long long)p.T * p.d, d, invmap,
-                             di.num_sms, stream, b.dH_parts));
+                             di.num_sms, stream, b.dH_parts, true));
   return KD_OK;
 }
 

@@ -28,23 +28,26 @@ cudaError_t launch_kernel(const char* name, void (*kern)(KArgs...), dim3 grid, d
   return e;
 }
 
-// Same, launched as clusters of `cluster_x` CTAs along x.
+// Same, launched as clusters of `cluster_x` CTAs along x, and (early) allowed to
+// start before the launch ahead of it has ended (see launch_kernel_early).
 template <typename... KArgs, typename... Args>
 cudaError_t launch_kernel_cluster(const char* name, void (*kern)(KArgs...), dim3 grid, dim3 block,
-                                  size_t smem, cudaStream_t stream, unsigned cluster_x,
+                                  size_t smem, cudaStream_t stream, unsigned cluster_x, bool early,
                                   Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = cluster_x;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = early ? 2 : 1;
   void* token = nullptr;
   note_launch_begin(name, stream, &token);
   cudaError_t e = cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
@@ -109,7 +112,8 @@ cudaError_t launch_loss_finalize(const double* block_sums, int nblocks, const in
 // out [T, d] bf16 <- in rows (invmap[t], or t when invmap is nullptr; zeros
 // for invmap[t] < 0); n = T * d; the sum of `parts` such arrays, n apart.
 cudaError_t launch_f32_to_bf16(const float* in, uint16_t* out, long long n, int d,
-                               const int* invmap, int num_sms, cudaStream_t stream, int parts = 1);
+                               const int* invmap, int num_sms, cudaStream_t stream, int parts = 1,
+                               bool early = false);
 // merge of per-split top-K lists; shared memory = topk_merge_p2() * 8 bytes
 int topk_merge_p2(int nsplit, int K);
 cudaError_t launch_topk_merge(const float* unit_val, const int32_t* unit_id, const int* unit_cnt,
@@ -156,10 +160,11 @@ int pair_max_active_clusters();
 
 // bn: N tile width (LOGIT_BN for the logit GEMMs; 256 for dH/dW).
 // pair: 2-CTA clusters sharing one 256 x bn tile (grid must be even).
+// early: see launch_kernel_early; the launch ahead is one of this library's.
 cudaError_t launch_gemm(GemmKind kind, int bn, bool pair, const CUtensorMap& tmA,
                         const CUtensorMap& tmB,
                         const GemmShape& sh, const EpiParams& ep, int* status, int grid,
-                        cudaStream_t stream);
+                        cudaStream_t stream, bool early = false);
 
 // dW (A = G^T, B = H, both MN-major) and dH (A = G K-major, B = W MN-major)
 // of one backward block in one persistent launch, their units in one
@@ -168,7 +173,8 @@ cudaError_t launch_gemm_dw_dh(bool pair, bool dh_first, const CUtensorMap& tmG_M
                               const CUtensorMap& tmH_MN, const GemmShape& sh_dw,
                               const EpiParams& ep_dw, const CUtensorMap& tmG_K,
                               const CUtensorMap& tmW_MN, const GemmShape& sh_dh,
-                              const EpiParams& ep_dh, int* status, int grid, cudaStream_t stream);
+                              const EpiParams& ep_dh, int* status, int grid, cudaStream_t stream,
+                              bool early = false);
 
 // kernels_small.cu, for the token log-probabilities
 // Compaction of the tokens whose gradient is not zero (NaN included).

@@ -16,7 +16,7 @@ template <int EPI, bool A_MN, bool B_MN, int BN, bool PAIR, bool DUAL>
 cudaError_t launch_one(const char* name, const CUtensorMap& tmA, const CUtensorMap& tmB,
                        const CUtensorMap& tmA1, const CUtensorMap& tmB1, const GemmShape& sh,
                        const GemmShape& sh1, const EpiParams& ep, const EpiParams& ep1,
-                       int* status, int grid, cudaStream_t stream) {
+                       int* status, int grid, cudaStream_t stream, bool early) {
   auto kern = tc_gemm_kernel<EPI, A_MN, B_MN, BN, PAIR, DUAL>;
   constexpr int smem = TileCfg<BN, PAIR>::SMEM_BYTES;
   // Per device and instantiation; concurrent first calls may both set the
@@ -33,9 +33,12 @@ cudaError_t launch_one(const char* name, const CUtensorMap& tmA, const CUtensorM
   }
   if (PAIR)
     return launch_kernel_cluster(name, kern, dim3(grid), dim3(GEMM_THREADS), (size_t)smem, stream,
-                                 2u, tmA, tmB, tmA1, tmB1, sh, sh1, ep, ep1, status);
-  return launch_kernel(name, kern, dim3(grid), dim3(GEMM_THREADS), (size_t)smem, stream, tmA,
-                       tmB, tmA1, tmB1, sh, sh1, ep, ep1, status);
+                                 2u, early, tmA, tmB, tmA1, tmB1, sh, sh1, ep, ep1, status);
+  if (!early)
+    return launch_kernel(name, kern, dim3(grid), dim3(GEMM_THREADS), (size_t)smem, stream, tmA,
+                         tmB, tmA1, tmB1, sh, sh1, ep, ep1, status);
+  return launch_kernel_cluster(name, kern, dim3(grid), dim3(GEMM_THREADS), (size_t)smem, stream,
+                               1u, early, tmA, tmB, tmA1, tmB1, sh, sh1, ep, ep1, status);
 }
 
 // One job per launch: the second job's parameters repeat the first's and are
@@ -43,12 +46,12 @@ cudaError_t launch_one(const char* name, const CUtensorMap& tmA, const CUtensorM
 template <int EPI, bool A_MN, bool B_MN, int BN>
 cudaError_t launch_pick(bool pair, const char* name, const CUtensorMap& tmA, const CUtensorMap& tmB,
                         const GemmShape& sh, const EpiParams& ep, int* status, int grid,
-                        cudaStream_t stream) {
+                        cudaStream_t stream, bool early) {
   if (pair)
     return launch_one<EPI, A_MN, B_MN, BN, true, false>(name, tmA, tmB, tmA, tmB, sh, sh, ep, ep,
-                                                        status, grid, stream);
+                                                        status, grid, stream, early);
   return launch_one<EPI, A_MN, B_MN, BN, false, false>(name, tmA, tmB, tmA, tmB, sh, sh, ep, ep,
-                                                       status, grid, stream);
+                                                       status, grid, stream, early);
 }
 
 }  // namespace
@@ -85,37 +88,37 @@ int pair_max_active_clusters() {
 
 cudaError_t launch_gemm(GemmKind kind, int bn, bool pair, const CUtensorMap& tmA,
                         const CUtensorMap& tmB, const GemmShape& sh, const EpiParams& ep,
-                        int* status, int grid, cudaStream_t stream) {
+                        int* status, int grid, cudaStream_t stream, bool early) {
   if (pair && (grid % 2) != 0) return cudaErrorInvalidValue;
   switch (kind) {
     case GEMM_FWD_LSE:
       if (bn != LOGIT_BN) break;
       return launch_pick<EPI_LSE, false, false, LOGIT_BN>(pair, "fwd_lse_gemm", tmA, tmB, sh, ep,
-                                                          status, grid, stream);
+                                                          status, grid, stream, early);
     case GEMM_BWD_GRAD:
       if (bn != LOGIT_BN) break;
       return launch_pick<EPI_GRAD, false, false, LOGIT_BN>(pair, "bwd_grad_gemm", tmA, tmB, sh,
-                                                           ep, status, grid, stream);
+                                                           ep, status, grid, stream, early);
     case GEMM_FWD_LSE_MIX:
       if (bn != LOGIT_BN) break;
       return launch_pick<EPI_LSE_MIX, false, false, LOGIT_BN>(pair, "fwd_lse_mix_gemm", tmA, tmB,
-                                                              sh, ep, status, grid, stream);
+                                                              sh, ep, status, grid, stream, early);
     case GEMM_BWD_GRAD_MIX:
       if (bn != LOGIT_BN) break;
       return launch_pick<EPI_GRAD_MIX, false, false, LOGIT_BN>(pair, "bwd_grad_mix_gemm", tmA,
-                                                               tmB, sh, ep, status, grid, stream);
+                                                               tmB, sh, ep, status, grid, stream, early);
     case GEMM_TOPK:
       if (bn != LOGIT_BN) break;
       return launch_pick<EPI_TOPK, false, false, LOGIT_BN>(pair, "topk_gemm", tmA, tmB, sh, ep,
-                                                           status, grid, stream);
+                                                           status, grid, stream, early);
     case GEMM_DH:
       if (bn != 256) break;
       return launch_pick<EPI_STORE, false, true, 256>(pair, "dH_gemm", tmA, tmB, sh, ep, status,
-                                                      grid, stream);
+                                                      grid, stream, early);
     case GEMM_DW:
       if (bn != 256) break;
       return launch_pick<EPI_STORE, true, true, 256>(pair, "dW_gemm", tmA, tmB, sh, ep, status,
-                                                     grid, stream);
+                                                     grid, stream, early);
   }
   return cudaErrorInvalidValue;
 }
@@ -124,24 +127,24 @@ cudaError_t launch_gemm_dw_dh(bool pair, bool dh_first, const CUtensorMap& tmG_M
                               const CUtensorMap& tmH_MN, const GemmShape& sh_dw,
                               const EpiParams& ep_dw, const CUtensorMap& tmG_K,
                               const CUtensorMap& tmW_MN, const GemmShape& sh_dh,
-                              const EpiParams& ep_dh, int* status, int grid, cudaStream_t stream) {
+                              const EpiParams& ep_dh, int* status, int grid, cudaStream_t stream, bool early) {
   if (pair && (grid % 2) != 0) return cudaErrorInvalidValue;
   if (dh_first) {  // job 0 = dH (A K-major), job 1 = dW
     if (pair)
       return launch_one<EPI_STORE, false, true, 256, true, true>(
           "dW_dH_gemm", tmG_K, tmW_MN, tmG_MN, tmH_MN, sh_dh, sh_dw, ep_dh, ep_dw, status, grid,
-          stream);
+          stream, early);
     return launch_one<EPI_STORE, false, true, 256, false, true>(
         "dW_dH_gemm", tmG_K, tmW_MN, tmG_MN, tmH_MN, sh_dh, sh_dw, ep_dh, ep_dw, status, grid,
-        stream);
+        stream, early);
   }
   if (pair)  // job 0 = dW (A MN-major), job 1 = dH
     return launch_one<EPI_STORE, true, true, 256, true, true>(
         "dW_dH_gemm", tmG_MN, tmH_MN, tmG_K, tmW_MN, sh_dw, sh_dh, ep_dw, ep_dh, status, grid,
-        stream);
+        stream, early);
   return launch_one<EPI_STORE, true, true, 256, false, true>(
       "dW_dH_gemm", tmG_MN, tmH_MN, tmG_K, tmW_MN, sh_dw, sh_dh, ep_dw, ep_dh, status, grid,
-      stream);
+      stream, early);
 }
 
 }  // namespace kdkl

@@ -170,15 +170,6 @@ __device__ __forceinline__ int run_length(int T, int warps) {
                ((long long)warps * SEQ_PIECE)) * SEQ_PIECE;
 }
 
-// Launches that follow one another closely: the next one's blocks may start
-// (up to their wait) while this one runs.
-__device__ __forceinline__ void grid_dependents_go() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-// Waits until the launches before this one are complete and their writes seen.
-__device__ __forceinline__ void grid_dependency_wait() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
 __device__ __forceinline__ void prefetch_l2(const void* p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }

@@ -408,11 +408,12 @@ __global__ void __launch_bounds__(1024)
 // out row t = bf16(in row invmap[t]), or zeros when invmap[t] < 0; invmap
 // nullptr: row t. One block per row at a time, d4 = d / 4 float4 per row. With
 // more than one part (part_stride4 float4 apart) the row is their sum, in order.
-__global__ void f32_to_bf16_kernel(const float4* __restrict__ in, uint2* __restrict__ out, int T,
-                                   int d4, const int* __restrict__ invmap, int parts,
-                                   long long part_stride4) {
+// (Not __restrict__: the loads must stay behind the wait.)
+__global__ void f32_to_bf16_kernel(const float4* in, uint2* out, int T, int d4, const int* invmap,
+                                   int parts, long long part_stride4) {
+  grid_dependency_wait();
   for (int t = blockIdx.x; t < T; t += gridDim.x) {
-    const int r = invmap ? __ldg(invmap + t) : t;
+    const int r = invmap ? invmap[t] : t;
     uint2* o = out + (long long)t * d4;
     if (r < 0) {
       for (int c = threadIdx.x; c < d4; c += blockDim.x) o[c] = make_uint2(0u, 0u);
@@ -447,6 +448,7 @@ template <typename M>
 __global__ void __launch_bounds__(SCAN_THREADS)
     mask_scan_kernel(const M* __restrict__ mask, int T, int* __restrict__ rowmap,
                      int* __restrict__ invmap, int* __restrict__ n_count) {
+  grid_dependents_go();
   __shared__ int warp_base[SCAN_THREADS / 32];
   __shared__ int tile_total;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -511,10 +513,11 @@ __global__ void __launch_bounds__(SCAN_THREADS)
 // before scaling, H row . W row in fp32 (a lane's products, then a tree).
 __global__ void __launch_bounds__(256)
     token_rows_kernel(const uint4* __restrict__ H, const uint4* __restrict__ W, int row16,
-                      const int32_t* __restrict__ ids, const int* __restrict__ rowmap,
-                      const int* __restrict__ n_count, int T, int V, int round,
-                      uint4* __restrict__ Hc, int32_t* __restrict__ sidx, float* __restrict__ sp,
-                      float* __restrict__ zdot, int* __restrict__ status) {
+                      const int32_t* __restrict__ ids, const int* rowmap, const int* n_count, int T,
+                      int V, int round, uint4* Hc, int32_t* sidx, float* sp, float* zdot,
+                      int* status) {
+  grid_dependents_go();
+  grid_dependency_wait();
   const int lane = threadIdx.x & 31;
   const int N = rowmap ? min(*n_count, T) : T;
   const long long end = Hc ? ((long long)N + round - 1) / round * round : N;
@@ -526,7 +529,7 @@ __global__ void __launch_bounds__(256)
       for (int c = lane; c < row16; c += 32) o[c] = make_uint4(0u, 0u, 0u, 0u);
       continue;
     }
-    const int tok = rowmap ? __ldg(rowmap + r) : (int)r;
+    const int tok = rowmap ? rowmap[r] : (int)r;
     const int id = __ldg(ids + tok);
     const bool known = id >= 0 && id < V;
     if (lane == 0) {
@@ -573,10 +576,10 @@ __global__ void __launch_bounds__(256)
 // fixed order. invmap as in lse_combine.
 template <int TOK>
 __global__ void __launch_bounds__(COMBINE_THREADS)
-    logp_combine_kernel(const float* __restrict__ pm, const float* __restrict__ ps,
-                        const float* __restrict__ pd, int nsplit, int T,
-                        const int* __restrict__ invmap, const float* __restrict__ zdot, float cl2,
-                        float inv_tau, float* __restrict__ logp, float* __restrict__ lse) {
+    logp_combine_kernel(const float* pm, const float* ps, const float* pd, int nsplit, int T,
+                        const int* invmap, const float* zdot, float cl2, float inv_tau, float* logp,
+                        float* lse) {
+  grid_dependency_wait();
   constexpr int STRANDS = COMBINE_THREADS / TOK;
   const int i = threadIdx.x % TOK, w = threadIdx.x / TOK;
   const int t = blockIdx.x * TOK + i;
@@ -930,9 +933,14 @@ cudaError_t launch_gather_rows(const uint16_t* H, int d, const int* rowmap, cons
 }
 
 cudaError_t launch_f32_to_bf16(const float* in, uint16_t* out, long long n, int d,
-                               const int* invmap, int num_sms, cudaStream_t stream, int parts) {
+                               const int* invmap, int num_sms, cudaStream_t stream, int parts,
+                               bool early) {
   const int T = (int)(n / d);  // n = T * d, d a multiple of 8
   const int blocks = std::max(1, std::min(T, num_sms * 8));
+  if (early)
+    return launch_kernel_early("f32_to_bf16", f32_to_bf16_kernel, dim3((unsigned)blocks), dim3(256),
+                               stream, reinterpret_cast<const float4*>(in),
+                               reinterpret_cast<uint2*>(out), T, d / 4, invmap, parts, n / 4);
   return launch_kernel("f32_to_bf16", f32_to_bf16_kernel, dim3((unsigned)blocks), dim3(256), 0,
                        stream, reinterpret_cast<const float4*>(in), reinterpret_cast<uint2*>(out),
                        T, d / 4, invmap, parts, n / 4);
@@ -949,10 +957,16 @@ cudaError_t launch_token_rows(const uint16_t* H, const uint16_t* W, int d, const
                               uint16_t* Hc, int32_t* sidx, float* sp, float* zdot, int* status,
                               int num_sms, cudaStream_t stream) {
   const int blocks = std::min((T + (Hc ? round : 0) + 7) / 8, num_sms * 8);
+  const uint4* h = reinterpret_cast<const uint4*>(H);
+  const uint4* w = reinterpret_cast<const uint4*>(W);
+  uint4* hc = reinterpret_cast<uint4*>(Hc);
+  if (rowmap)  // the scan that wrote it is ahead; without one, nothing of this call's is
+    return launch_kernel_early("token_rows", token_rows_kernel, dim3((unsigned)blocks), dim3(256),
+                               stream, h, w, d / 8, ids, rowmap, n_count, T, V, round, hc, sidx, sp,
+                               zdot, status);
   return launch_kernel("token_rows", token_rows_kernel, dim3((unsigned)blocks), dim3(256), 0,
-                       stream, reinterpret_cast<const uint4*>(H), reinterpret_cast<const uint4*>(W),
-                       d / 8, ids, rowmap, n_count, T, V, round, reinterpret_cast<uint4*>(Hc), sidx,
-                       sp, zdot, status);
+                       stream, h, w, d / 8, ids, rowmap, n_count, T, V, round, hc, sidx, sp, zdot,
+                       status);
 }
 
 cudaError_t launch_logp_combine(const float* pm, const float* ps, const float* pd, int nsplit,
@@ -960,11 +974,11 @@ cudaError_t launch_logp_combine(const float* pm, const float* ps, const float* p
                                 float inv_tau, float* logp, float* lse, cudaStream_t stream) {
   // Few tokens: more threads on each one's splits, and more blocks.
   if (T <= 4096)
-    return launch_kernel("logp_combine", logp_combine_kernel<4>, dim3((T + 3) / 4),
-                         dim3(COMBINE_THREADS), 0, stream, pm, ps, pd, nsplit, T, invmap,
+    return launch_kernel_early("logp_combine", logp_combine_kernel<4>, dim3((T + 3) / 4),
+                               dim3(COMBINE_THREADS), stream, pm, ps, pd, nsplit, T, invmap,
                          zdot, cl2, inv_tau, logp, lse);
-  return launch_kernel("logp_combine", logp_combine_kernel<32>, dim3((T + 31) / 32),
-                       dim3(COMBINE_THREADS), 0, stream, pm, ps, pd, nsplit, T, invmap,
+  return launch_kernel_early("logp_combine", logp_combine_kernel<32>, dim3((T + 31) / 32),
+                             dim3(COMBINE_THREADS), stream, pm, ps, pd, nsplit, T, invmap,
                        zdot, cl2, inv_tau, logp, lse);
 }
 

@@ -404,30 +404,10 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
   auto ufull_bar = [&](int i) { return bar0 + 8u * (2 * STAGES + 5 + i); };
   auto uempty_bar = [&](int i) { return bar0 + 8u * (2 * STAGES + 5 + NSLOT + i); };
 
-  // Every role shrinks the shapes to the live rows the same way, so they all
-  // see the same units and K steps.
-  GemmShape sh = sh_in;
-  GemmShape sh1 = sh1_in;
-  int live_rows = IS_LSE || IS_GRAD ? ep.rows : 0;  // rows whose token counts
-  {
-    const int a = shrink_shape<TILE_M>(sh);
-    if (a >= 0) live_rows = min(live_rows, a);
-    if (DUAL) shrink_shape<TILE_M>(sh1);
-  }
-  const int units0 = sh.units;
-  const int units_all = units0 + (DUAL ? sh1.units : 0);
-  // Per unit: its job's shape, the unit within that job, and A's layout.
-  auto job_of = [&](int u, const GemmShape*& js, int& uu, bool& a_mn) {
-    const bool j1 = DUAL && u >= units0;
-    js = j1 ? &sh1 : &sh;
-    uu = j1 ? u - units0 : u;
-    a_mn = j1 ? !A_MN : A_MN;
-    return j1;
-  };
-
+  grid_dependents_go();
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const uint64_t limit = sh.inject_stall ? kInjectedWaitLimitNs : kWaitLimitNs;
+  const uint64_t limit = sh_in.inject_stall ? kInjectedWaitLimitNs : kWaitLimitNs;
   // PAIR: CTAs 2c and 2c+1 form cluster c; rank 0 (the leader) issues the MMAs.
   const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
   const bool leader = rank == 0;
@@ -475,6 +455,29 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
   if (PAIR) cluster_sync_all();  // the peer's barriers exist before any remote arrive
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+
+  // Up to here nothing was read that an earlier launch writes.
+  grid_dependency_wait();
+  // Every role shrinks the shapes to the live rows the same way, so they all
+  // see the same units and K steps.
+  GemmShape sh = sh_in;
+  GemmShape sh1 = sh1_in;
+  int live_rows = IS_LSE || IS_GRAD ? ep.rows : 0;  // rows whose token counts
+  {
+    const int a = shrink_shape<TILE_M>(sh);
+    if (a >= 0) live_rows = min(live_rows, a);
+    if (DUAL) shrink_shape<TILE_M>(sh1);
+  }
+  const int units0 = sh.units;
+  const int units_all = units0 + (DUAL ? sh1.units : 0);
+  // Per unit: its job's shape, the unit within that job, and A's layout.
+  auto job_of = [&](int u, const GemmShape*& js, int& uu, bool& a_mn) {
+    const bool j1 = DUAL && u >= units0;
+    js = j1 ? &sh1 : &sh;
+    uu = j1 ? u - units0 : u;
+    a_mn = j1 ? !A_MN : A_MN;
+    return j1;
+  };
 
   // Consumer side of the unit ring: wait for slot q's unit (cluster-scope
   // acquire with a pair: the leader wrote the peer's slot remotely), then

@@ -113,6 +113,19 @@ __device__ __forceinline__ bool mbar_drain_bounded(uint32_t bar, uint32_t parity
   }
 }
 
+// ------------------------------------------- launches that follow one another
+
+// The next launch's blocks may start (up to their wait) while this one runs, if
+// it was launched to (launch_kernel_early); nothing otherwise.
+__device__ __forceinline__ void grid_dependents_go() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+// Waits until the launches before this one are complete and their writes seen;
+// nothing for a launch that started after them anyway.
+__device__ __forceinline__ void grid_dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // ----------------------------------------------------------------------- TMA
 
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* tm) {
