@@ -199,10 +199,11 @@ struct PolicyArgs {
   float inv_norm, kl_coef, grad_loss;
   float r_low, r_high, r_dual;                                       // clipped ratios
   float low_hi, low_lo, high_hi, high_lo, dual_hi, dual_lo;          // borders of logp - old_logp
-  int* n_count;        // [0] counted tokens, [1] sequences that have any, [2] clipped tokens
+  int* n_count;        // [0] counted tokens, [1] sequences that have any
   int* n_seq;          // [S] counted tokens of each sequence
   int* ticket;         // blocks done
   float4* block_part;  // [blocks] the two sums, each in two floats
+  int* block_clips;    // [blocks]
   float *loss, *stats, *grad;
 };
 struct PrefArgs {

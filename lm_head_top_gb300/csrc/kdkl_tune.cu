@@ -11,7 +11,7 @@
 namespace kdkl {
 namespace {
 
-constexpr size_t kHeader = 256;  // int status; three counts; a ticket
+constexpr size_t kHeader = 256;  // int status; two counts; a ticket
 // Bound on the SM count that sizes workspaces (the same with and without a device).
 constexpr int kMaxSms = 256;
 constexpr int64_t kMaxTokens = (1ll << 31) - 4096;  // a block's token indexes stay in 31 bits
@@ -38,13 +38,14 @@ void split_border(double x, float* hi, float* lo) {
 }
 
 struct PolicyLayout {
-  size_t off_seq, off_part, total;
+  size_t off_seq, off_part, off_clips, total;
 };
 PolicyLayout policy_layout(const kd_policy_problem& p) {
   PolicyLayout L{};
   L.off_seq = kHeader;
   L.off_part = pad256(L.off_seq + (size_t)p.S * 4);
-  L.total = pad256(L.off_part + (size_t)seq_blocks((int)p.T, kMaxSms) * 16);
+  L.off_clips = pad256(L.off_part + (size_t)seq_blocks((int)p.T, kMaxSms) * 16);
+  L.total = pad256(L.off_clips + (size_t)seq_blocks((int)p.T, kMaxSms) * 4);
   return L;
 }
 
@@ -162,6 +163,7 @@ kd_status kd_policy_loss(const kd_policy_problem* prob, const float* logp, const
   a.n_seq = place<int>(workspace, L.off_seq);
   a.ticket = status + 4;
   a.block_part = place<float4>(workspace, L.off_part);
+  a.block_clips = place<int>(workspace, L.off_clips);
   a.loss = loss;
   a.stats = stats;
   a.grad = grad_logp;

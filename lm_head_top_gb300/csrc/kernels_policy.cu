@@ -14,10 +14,16 @@
 // are joined in a fixed order (no floating-point atomics): the results do not
 // change from run to run.
 //
-// What bounds both on long batches: DRAM (17 bytes a token for the policy loss
-// with per-sequence advantages, 13 for the preference loss, whose gradient pass
-// reads the mask once more). On short ones: the launches, so a batch that one
-// block can hold takes one launch.
+// What bounds them. Their bytes are 17 a token for the policy loss with an
+// advantage per sequence (21 with one per token) and 13 for the preference loss,
+// whose gradient pass reads the mask once more. On short batches it is the
+// launches: a batch that one block can hold takes one. In between it is chains of
+// dependent lookups, joins and starts, about 10 us a launch. On 8.4M tokens the
+// policy loss takes 42 us after a count of 9 (21 at the copy rate): the SMs issue
+// 2.3 of 4 instructions a cycle, half of them on the pipe for comparisons and
+// selections. Not the lever there: 128 or 256 tokens a piece, 16 to 40 warps an
+// SM, runs by block instead of by warp, the next piece's loads ahead of the
+// arithmetic, arithmetic without branches; each measured within 10 %.
 #include <cuda_bf16.h>
 #include <math.h>
 #include <stdint.h>
@@ -31,12 +37,12 @@ namespace kdkl {
 
 namespace {
 
-constexpr int SEQ_THREADS = 256;
+constexpr int SEQ_THREADS = 512;
 constexpr int SEQ_WARPS = SEQ_THREADS / 32;
 constexpr int SEQ_TOK = 4;              // consecutive tokens per lane: a 16-byte load
 constexpr int SEQ_PIECE = 32 * SEQ_TOK;  // tokens of a warp's step
-constexpr int SEQ_RESIDENT = 5;          // blocks of a walk on an SM
-constexpr int PREF_ONE_THREADS = 512;   // the one-block preference loss
+constexpr int SEQ_RESIDENT = 2;          // blocks of a walk on an SM
+constexpr int PREF_ONE_THREADS = 512;    // the one-block preference loss
 
 // First sequence in [lo, lo + n) whose end is past token t (the last one if
 // none is), found by the whole warp: 32 probes a step.
@@ -71,10 +77,11 @@ __device__ __noinline__ int seq_advance(const int32_t* cu, int S, int s, int t) 
   return lo;
 }
 
-// A lane's consecutive values from token t on; those at or past T read as zero.
-__device__ __forceinline__ void load_tok(const float* p, int t, int T, bool vec,
+// A lane's consecutive values from token t on. whole: aligned, and all of them
+// exist; else those at or past T read as zero.
+__device__ __forceinline__ void load_tok(const float* p, int t, int T, bool whole,
                                          float (&x)[SEQ_TOK]) {
-  if (vec && t + SEQ_TOK <= T) {
+  if (whole) {
     const float4 a = __ldg(reinterpret_cast<const float4*>(p + t));
     x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
   } else {
@@ -83,9 +90,9 @@ __device__ __forceinline__ void load_tok(const float* p, int t, int T, bool vec,
   }
 }
 
-__device__ __forceinline__ void store_tok(float* p, int t, int T, bool vec,
+__device__ __forceinline__ void store_tok(float* p, int t, int T, bool whole,
                                           const float (&x)[SEQ_TOK]) {
-  if (vec && t + SEQ_TOK <= T) {
+  if (whole) {
     *reinterpret_cast<float4*>(p + t) = make_float4(x[0], x[1], x[2], x[3]);
   } else {
 #pragma unroll
@@ -271,13 +278,13 @@ __device__ __forceinline__ float exp_rest(float x) {
 template <bool NEED_SEQ>
 __global__ void __launch_bounds__(SEQ_THREADS, SEQ_RESIDENT)
     policy_loss_kernel(const PolicyArgs a, int* status) {
-  __shared__ int count, clips;
+  __shared__ int count, any, clips;
   __shared__ float2 part[2][SEQ_WARPS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool alone = gridDim.x == 1;
   const bool vec = a.vec != 0;
   if (threadIdx.x == 0) {
-    count = clips = 0;
+    count = any = clips = 0;
     if (alone) *status = 0;  // with more blocks the call has cleared it
   }
   __syncthreads();
@@ -298,20 +305,22 @@ __global__ void __launch_bounds__(SEQ_THREADS, SEQ_RESIDENT)
   // Counted tokens: given (no mask), counted before, or counted here by every
   // block for itself (a short mask, which saves the launch that would count it).
   int n = a.T;
-  if (a.mask) {
-    if (a.count_here) {
-      int c = 0;
-      for (int i = threadIdx.x * 16; i < a.T; i += SEQ_THREADS * 16)
-        c += __popc(load_mask16(a.mask, i, a.T, vec));
-      c = __reduce_add_sync(0xffffffffu, c);
-      if (lane == 0 && c) atomicAdd(&count, c);
-      __syncthreads();
-      n = count;
-    } else {
-      n = __ldcg(a.n_count);
-    }
+  if (a.mask && a.count_here) {
+    int c = 0;
+    for (int i = threadIdx.x * 16; i < a.T; i += SEQ_THREADS * 16)
+      c += __popc(load_mask16(a.mask, i, a.T, vec));
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (lane == 0 && c) atomicAdd(&count, c);
   }
-  const int n_any = a.reduction == 1 ? __ldcg(a.n_count + 1) : 0;
+  // One thread of a block reads the counts: every warp of the grid at the same
+  // line of L2 is a queue of its own (3 us of a large batch's 50).
+  if (threadIdx.x == 0) {
+    if (a.mask && !a.count_here) count = __ldcg(a.n_count);
+    if (a.reduction == 1) any = __ldcg(a.n_count + 1);
+  }
+  __syncthreads();
+  if (a.mask) n = count;
+  const int n_any = any;
   float w = a.reduction == 0 ? (n > 0 ? 1.f / (float)n : 0.f) : a.inv_norm;
   float w_adv = 0.f;  // the sequence's advantage
   auto enter = [&](int t) {  // the sequence of token t and its values
@@ -325,36 +334,41 @@ __global__ void __launch_bounds__(SEQ_THREADS, SEQ_RESIDENT)
   };
   if (NEED_SEQ) end = -1;  // enter at the first token
 
-  const float* ahead = lane < 4 ? a.logp : lane < 8 ? a.old_logp : lane < 12 ? a.ref_logp : nullptr;
-  if (lane >= 12 && lane < 16 && !a.adv_per_seq) ahead = a.advantages;
-  Sum2 pg, kl;
-  int clipped = 0;
+  Sum2 pg, kl;  // of the lane's sums over eight pieces, 32 tokens
+  float pg1 = 0.f, kl1 = 0.f;
+  int left = 8, clipped = 0;
   for (int p = begin; p < run_end; p += SEQ_PIECE) {
     const int t = p + lane * SEQ_TOK;
-    // a lane per line of a piece's arrays: the piece after the next one's way
-    // from memory starts two steps before it is needed
-    if (ahead && p + 2 * SEQ_PIECE + (lane & 3) * 32 < run_end)
-      prefetch_l2(ahead + p + 2 * SEQ_PIECE + (lane & 3) * 32);
     if (t >= run_end) break;  // nothing below is collective
     const uint32_t on = load_mask(a.mask, t, a.T, vec);
+    const bool whole = vec && t + SEQ_TOK <= a.T;
     float lp[SEQ_TOK], lo[SEQ_TOK], lr[SEQ_TOK], adv[SEQ_TOK];
-    load_tok(a.logp, t, a.T, vec, lp);
-    if (a.old_logp) load_tok(a.old_logp, t, a.T, vec, lo);
-    if (a.ref_logp) load_tok(a.ref_logp, t, a.T, vec, lr);
-    if (!a.adv_per_seq) load_tok(a.advantages, t, a.T, vec, adv);
+    if (whole) {  // one test for all the loads
+      load_tok(a.logp, t, a.T, true, lp);
+      if (a.old_logp) load_tok(a.old_logp, t, a.T, true, lo);
+      if (a.ref_logp) load_tok(a.ref_logp, t, a.T, true, lr);
+      if (!a.adv_per_seq) load_tok(a.advantages, t, a.T, true, adv);
+    } else {
+      load_tok(a.logp, t, a.T, false, lp);
+      if (a.old_logp) load_tok(a.old_logp, t, a.T, false, lo);
+      if (a.ref_logp) load_tok(a.ref_logp, t, a.T, false, lr);
+      if (!a.adv_per_seq) load_tok(a.advantages, t, a.T, false, adv);
+    }
     float g[SEQ_TOK];
 #pragma unroll
     for (int j = 0; j < SEQ_TOK; ++j) g[j] = 0.f;
-    float pg1 = 0.f, kl1 = 0.f;
     // The lane's tokens, a sequence at a time: once, but where one ends.
-    for (int at = t; at < min(t + SEQ_TOK, a.T);) {
+    int at = t;
+    do {
       uint32_t mine = on;
       int upto = t + SEQ_TOK;
       if (NEED_SEQ) {
         if (at >= end) enter(at);
         // (an end that is not past `at` comes of bad offsets: the last sequence's then)
-        if (end > at && end < upto) upto = end;
-        mine &= ((1u << (upto - t)) - 1u) & ~((1u << (at - t)) - 1u);
+        if (at > t || end < upto) {
+          if (end > at && end < upto) upto = end;
+          mine &= ((1u << (upto - t)) - 1u) & ~((1u << (at - t)) - 1u);
+        }
       }
       at = upto;
 #pragma unroll
@@ -392,11 +406,22 @@ __global__ void __launch_bounds__(SEQ_THREADS, SEQ_RESIDENT)
         clipped += clip ? 1 : 0;
         g[j] = fmaf(wj * a.grad_loss, gj, g[j]);
       }
+    } while (NEED_SEQ && at < min(t + SEQ_TOK, a.T));
+    if (a.grad) {
+      if (whole)
+        store_tok(a.grad, t, a.T, true, g);
+      else
+        store_tok(a.grad, t, a.T, false, g);
     }
-    if (a.grad) store_tok(a.grad, t, a.T, vec, g);
-    pg.add(pg1);
-    kl.add(kl1);
+    if (--left == 0) {
+      pg.add(pg1);
+      kl.add(kl1);
+      pg1 = kl1 = 0.f;
+      left = 8;
+    }
   }
+  pg.add(pg1);
+  kl.add(kl1);
   __syncwarp();
   pg = warp_sum(pg);
   kl = warp_sum(kl);
@@ -425,22 +450,24 @@ __global__ void __launch_bounds__(SEQ_THREADS, SEQ_RESIDENT)
     int done = 0;
     if (lane == 0) {
       a.block_part[blockIdx.x] = make_float4(pg.hi, pg.lo, kl.hi, kl.lo);
-      if (clipped) atomicAdd(a.n_count + 2, clipped);
+      a.block_clips[blockIdx.x] = clipped;
       __threadfence();
       done = atomicAdd(a.ticket, 1) == (int)gridDim.x - 1;
     }
     if (!__shfl_sync(0xffffffffu, done, 0)) return;
     __threadfence();
     pg = kl = Sum2();
+    clipped = 0;
 #pragma unroll 8
     for (int b = lane; b < (int)gridDim.x; b += 32) {
       const float4 v = __ldcg(a.block_part + b);
       pg.add(v.x, v.y);
       kl.add(v.z, v.w);
+      clipped += __ldcg(a.block_clips + b);
     }
     pg = warp_sum(pg);
     kl = warp_sum(kl);
-    clipped = __ldcg(a.n_count + 2);
+    clipped = __reduce_add_sync(0xffffffffu, clipped);
   }
   if (lane == 0) {
     Sum2 loss = pg;
@@ -481,9 +508,10 @@ __device__ __forceinline__ void pref_sums(const PrefArgs& a, int w, int R) {
   for (int p = (int)first; p < run_end; p += SEQ_PIECE) {
     const int t = p + lane * SEQ_TOK;
     const uint32_t on = load_mask(a.mask, t, a.T, a.vec != 0);
+    const bool whole = a.vec != 0 && t + SEQ_TOK <= a.T;
     float x[SEQ_TOK], y[SEQ_TOK];
-    load_tok(a.logp, t, a.T, a.vec != 0, x);
-    if (a.ref_logp) load_tok(a.ref_logp, t, a.T, a.vec != 0, y);
+    load_tok(a.logp, t, a.T, whole, x);
+    if (a.ref_logp) load_tok(a.ref_logp, t, a.T, whole, y);
 #pragma unroll
     for (int j = 0; j < SEQ_TOK; ++j)
       x[j] = (on >> j) & 1u ? (a.ref_logp ? x[j] - y[j] : x[j]) : 0.f;
@@ -608,7 +636,7 @@ __device__ __forceinline__ void pref_grads(const PrefArgs& a, int w, int R) {
       }
       g[j] = (on >> j) & 1u ? c : 0.f;
     }
-    store_tok(a.grad, t, a.T, a.vec != 0, g);
+    store_tok(a.grad, t, a.T, a.vec != 0 && t + SEQ_TOK <= a.T, g);
   }
 }
 
