@@ -344,15 +344,29 @@ double rmw_bytes(const BlockPlan& b, int64_t T, const kd_kl_problem& p) {
          ((double)(b.n_vblocks - 1) * (double)T + (double)(b.n_tblocks - 1) * (double)p.V);
 }
 
-// Parts of the dH product along a block's vocabulary: of few tokens it has fewer
+// Parts of the dH product along a block's vocabulary. Of few tokens it has fewer
 // 256 x 256 tiles than the 76 CTA pairs (12 for 640 tokens of d = 1000), each of
-// which then walks the whole vocabulary alone (32,003 columns: 208 us; in 10
-// parts 50). Enough parts for two units a pair, none shorter
-// than 8 steps of 64 columns.
+// which then walks the whole vocabulary alone, and a few more tiles than pairs
+// take two rounds (96 for 2048 tokens of d = 2880). In p parts, units of 1/p of
+// the steps go round ceil(tiles p / 76) times; each part costs the fp32 output
+// written and read once more, each round its last epilogue. The p of least time
+// by these (0.25 us a step of 64 columns, 5 TB/s, 2 us) is taken where it saves a
+// tenth: one part cost 208 us at 32,003 columns and 640 tokens of d = 1000, ten
+// 53, the four of this rule 41; 583 us at 64,000 columns and 2048 tokens of
+// d = 2880, the three of this rule 426.
 int dH_split(int64_t T, int64_t d, int64_t Vb) {
-  const int64_t tiles = ceil_div(T, 2 * BM) * ceil_div(d, 256);
-  if (tiles >= 76) return 1;
-  return (int)std::max<int64_t>(1, std::min(ceil_div(152, tiles), ceil_div(Vb, BK) / 8));
+  constexpr double kPairs = 76, kStepUs = 0.25, kBytesPerUs = 5e6, kRoundUs = 2;
+  const double tiles = (double)(ceil_div(T, 2 * BM) * ceil_div(d, 256));
+  const double steps = (double)ceil_div(Vb, BK);
+  auto time = [&](int p) {
+    const double rounds = std::ceil(tiles * p / kPairs);
+    return rounds / p * steps * kStepUs + p * 8.0 * (double)T * (double)d / kBytesPerUs +
+           rounds * kRoundUs;
+  };
+  int best = 1;
+  for (int p = 2; p <= 16 && p * 8 <= steps; ++p)
+    if (time(p) < time(best)) best = p;
+  return time(best) <= 0.9 * time(1) ? best : 1;
 }
 
 // own_teacher: the backward prepares the sorted teacher cache itself (sidx,
@@ -1305,10 +1319,9 @@ size_t kd_logprob_workspace_size(const kd_logprob_problem* prob, int which) {
   if (which != 0) return 0;
   DeviceInfo di;
   const int sms = (device_info(&di) == KD_OK) ? di.num_sms : 160;
-  size_t total = plan_logprob(p, sms, false, sms).total;
-  for (int procs = 1; procs <= sms / 2; ++procs)
-    total = std::max(total, plan_logprob(p, sms, true, procs).total);
-  return total;
+  // More processors, more splits: the most there can be of either tile size.
+  return std::max(plan_logprob(p, sms, false, sms).total,
+                  plan_logprob(p, sms, true, std::max(1, sms / 2)).total);
 }
 
 kd_status kd_logprob_forward(const kd_logprob_problem* prob, const uint16_t* H, const uint16_t* W,

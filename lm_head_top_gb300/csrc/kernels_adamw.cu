@@ -206,10 +206,6 @@ __device__ __forceinline__ float sqrt_approx(float x) {
   return y;
 }
 
-__device__ __forceinline__ void prefetch_l2(const void* p) {
-  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
-}
-
 // The lines of a warp's pass from element i on, a lane each: p, g, m and v
 // cover 256 elements in at most 8 + 8 + 2 + 2 lines of 128 bytes.
 template <typename P, typename G>

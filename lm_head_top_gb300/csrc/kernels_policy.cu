@@ -177,10 +177,6 @@ __device__ __forceinline__ int run_length(int T, int warps) {
                ((long long)warps * SEQ_PIECE)) * SEQ_PIECE;
 }
 
-__device__ __forceinline__ void prefetch_l2(const void* p) {
-  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
-}
-
 // --------------------------------------------------------------- policy loss
 
 // Counted tokens: of all into n_count[0]; with n_seq, of every sequence into

@@ -437,8 +437,9 @@ __global__ void f32_to_bf16_kernel(const float4* in, uint2* out, int T, int d4, 
 
 // Compaction of the counted tokens, one block: rowmap[r] = the r-th token
 // with mask != 0 (in order), invmap[t] = its r or -1, *n_count = N. The mask
-// is taken in tiles of 32 x 1024 tokens: warp w owns 32 consecutive 32-token
-// chunks of a tile and takes their ballots, eight loads in flight (lane j keeps
+// is taken in tiles of up to 32 x 1024 tokens: warp w owns up to 32 consecutive
+// 32-token chunks of a tile (fewer when the tokens are, so that all warps have
+// some) and takes their ballots, eight loads in flight (lane j keeps
 // chunk j's), a block scan gives each chunk its first row, and the maps are
 // written from the ballots. Loads and invmap stores are coalesced 32-token
 // pieces; chunks past the last token are passed over.
@@ -453,12 +454,13 @@ __global__ void __launch_bounds__(SCAN_THREADS)
   __shared__ int tile_total;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t below = (1u << lane) - 1u;
-  constexpr long long TILE = 32LL * SCAN_THREADS;  // tokens per tile
+  const int per_warp = (int)min(32ll, ((long long)T + SCAN_THREADS - 1) / SCAN_THREADS);
+  const long long TILE = (long long)per_warp * SCAN_THREADS;  // tokens per tile
   int base = 0;                                     // rows before this tile
   for (long long t0 = 0; t0 < T; t0 += TILE) {
-    const long long w0 = t0 + (long long)warp * 32 * 32;  // this warp's first token
+    const long long w0 = t0 + (long long)warp * per_warp * 32;  // this warp's first token
     // the warp's chunks that hold tokens
-    const int chunks = (int)max(0ll, min(32ll, (T - w0 + 31) / 32));
+    const int chunks = (int)max(0ll, min((long long)per_warp, (T - w0 + 31) / 32));
     uint32_t mine = 0;  // chunk `lane`'s ballot
 #pragma unroll 8
     for (int j = 0; j < chunks; ++j) {

@@ -355,6 +355,12 @@ __device__ __forceinline__ void tc_commit_pair_local(uint32_t bar) {
                : "memory");
 }
 
+// ------------------------------------------------------------------ memory
+
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
 // ------------------------------------------------------------------- math
 
 // Hardware base-2 exponential (MUFU); flushes subnormal results to zero.

@@ -163,3 +163,23 @@ def test_large_vocabulary_rows(kdkl, T):
     ref = torch.logsumexp(z, 1)
     assert (lse - ref).abs().max().item() <= LSE_ATOL
     assert (logp - (z.gather(1, ids.long()[:, None])[:, 0] - ref)).abs().max().item() <= LSE_ATOL
+
+
+@pytest.mark.parametrize("T", [1024, 1025, 32768, 32769, 70001])
+def test_compaction_over_many_tokens(kdkl, T):
+    """Token counts around the compaction's tiles, most tokens without a gradient."""
+    d, V = 8, 40
+    H, W, ids, mask, grad = _make(T, d, V, seed=5, off=0.9)
+    g = [t.cuda() for t in (H, W, ids, mask, grad)]
+    logp, lse = kdkl.kd_logprob_forward(*g[:4])
+    dH, dW = kdkl.kd_logprob_backward(*g[:3], lse, g[4])
+    z = g[0].double() @ g[1].double().t()
+    on = g[3] != 0
+    ref = torch.where(on, z.gather(1, g[2].long()[:, None])[:, 0] - torch.logsumexp(z, 1), 0.0)
+    assert (logp - ref).abs().max().item() <= LSE_ATOL
+    slope = -torch.softmax(z, 1)
+    slope[torch.arange(T, device="cuda"), g[2].long()] += 1
+    slope *= g[4].double()[:, None]
+    assert rel_l2(dH.float().cpu().numpy(), (slope @ g[1].double()).cpu().numpy()) <= GRAD_TOL
+    assert rel_l2(dW.cpu().numpy(), (slope.t() @ g[0].double()).cpu().numpy()) <= GRAD_TOL
+    assert not dH[~on].any()
