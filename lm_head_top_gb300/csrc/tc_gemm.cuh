@@ -1052,7 +1052,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
         if (no_k) continue;  // no accumulator was used
         if (lane == 0) {
           if (PAIR)
-            mbar_arrive_cluster(tempty_remote0 + 8u * acc);  // the leader's barrier
+            mbar_arrive_cluster_tmem(tempty_remote0 + 8u * acc);  // the leader's barrier
           else
             mbar_arrive(tempty_bar(acc));
         }

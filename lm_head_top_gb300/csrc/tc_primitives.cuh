@@ -266,6 +266,15 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
                : "memory");
 }
 
+// The same without waiting for this thread's global stores to be seen by the
+// cluster (release at CTA scope): for a barrier that hands on nothing in memory,
+// only a TMEM accumulator whose loads have completed (tcgen05.wait::ld, then
+// fence::before_thread_sync).
+__device__ __forceinline__ void mbar_arrive_cluster_tmem(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
+}
+
 // 32-bit store into shared memory of a CTA of this cluster (mapa address).
 __device__ __forceinline__ void st_shared_cluster_u32(uint32_t cluster_addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
