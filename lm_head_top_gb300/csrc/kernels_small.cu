@@ -408,9 +408,9 @@ __global__ void __launch_bounds__(1024)
 // out row t = bf16(in row invmap[t]), or zeros when invmap[t] < 0; invmap
 // nullptr: row t. One block per row at a time, d4 = d / 4 float4 per row. With
 // more than one part (part_stride4 float4 apart) the row is their sum, in order.
-// (Not __restrict__: the loads must stay behind the wait.)
-__global__ void f32_to_bf16_kernel(const float4* in, uint2* out, int T, int d4, const int* invmap,
-                                   int parts, long long part_stride4) {
+// (The inputs are not __restrict__: their loads must stay behind the wait.)
+__global__ void f32_to_bf16_kernel(const float4* in, uint2* __restrict__ out, int T, int d4,
+                                   const int* invmap, int parts, long long part_stride4) {
   grid_dependency_wait();
   for (int t = blockIdx.x; t < T; t += gridDim.x) {
     const int r = invmap ? invmap[t] : t;
@@ -420,6 +420,20 @@ __global__ void f32_to_bf16_kernel(const float4* in, uint2* out, int T, int d4, 
       continue;
     }
     const float4* src = in + (long long)r * d4;
+    if (parts == 1) {
+      for (int c0 = threadIdx.x; c0 < d4; c0 += 4 * blockDim.x) {  // four loads in flight
+        float4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (c0 + k * (int)blockDim.x < d4) v[k] = __ldcs(src + c0 + k * blockDim.x);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (c0 + k * (int)blockDim.x < d4)
+            o[c0 + k * blockDim.x] =
+                make_uint2(pack_bf16x2(v[k].x, v[k].y), pack_bf16x2(v[k].z, v[k].w));
+      }
+      continue;
+    }
     for (int c = threadIdx.x; c < d4; c += blockDim.x) {
       float4 v = src[c];
 #pragma unroll 4
@@ -462,12 +476,18 @@ __global__ void __launch_bounds__(SCAN_THREADS)
     // the warp's chunks that hold tokens
     const int chunks = (int)max(0ll, min((long long)per_warp, (T - w0 + 31) / 32));
     uint32_t mine = 0;  // chunk `lane`'s ballot
-#pragma unroll 8
-    for (int j = 0; j < chunks; ++j) {
-      const long long t = w0 + (long long)j * 32 + lane;
-      const bool on = t < T && mask[t] != (M)0;
-      const uint32_t b = __ballot_sync(0xffffffffu, on);
-      if (lane == j) mine = b;
+    for (int j0 = 0; j0 < chunks; j0 += 8) {
+      bool on[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const long long t = w0 + (long long)(j0 + k) * 32 + lane;
+        on[k] = j0 + k < chunks && t < T && mask[t] != (M)0;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t b = __ballot_sync(0xffffffffu, on[k]);
+        if (lane == j0 + k) mine = b;
+      }
     }
     const int my_count = __popc(mine);
     int incl = my_count;  // chunks of this warp, in order
@@ -491,6 +511,7 @@ __global__ void __launch_bounds__(SCAN_THREADS)
     }
     __syncthreads();
     const int chunk_first = base + warp_base[warp] + incl - my_count;  // chunk `lane`'s first row
+#pragma unroll 4
     for (int j = 0; j < chunks; ++j) {
       const long long t = w0 + (long long)j * 32 + lane;
       const uint32_t b = __shfl_sync(0xffffffffu, mine, j);
