@@ -19,11 +19,11 @@
 // whose gradient pass reads the mask once more. On short batches it is the
 // launches: a batch that one block can hold takes one. In between it is chains of
 // dependent lookups, joins and starts, about 10 us a launch. On 8.4M tokens the
-// policy loss takes 42 us after a count of 9 (21 at the copy rate): the SMs issue
-// 2.3 of 4 instructions a cycle, half of them on the pipe for comparisons and
-// selections. Not the lever there: 128 or 256 tokens a piece, 16 to 40 warps an
-// SM, runs by block instead of by warp, the next piece's loads ahead of the
-// arithmetic, arithmetic without branches; each measured within 10 %.
+// policy loss takes 42 us after a count of 9 (21 at the copy rate): 96
+// instructions a token at 2.0 of 4 a cycle, half of the stalls waits for loads.
+// Not the lever there: 128 or 256 tokens a piece, 16 to 40 warps an SM, runs by
+// block instead of by warp, the next piece prefetched to L2 or to registers,
+// arithmetic without branches; each measured within 10 %.
 #include <cuda_bf16.h>
 #include <math.h>
 #include <stdint.h>
