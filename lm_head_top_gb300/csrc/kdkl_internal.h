@@ -63,10 +63,11 @@ cudaError_t launch_kernel_cluster(const char* name, void (*kern)(KArgs...), dim3
 // two launches orders them fully.)
 template <typename... KArgs, typename... Args>
 cudaError_t launch_kernel_early(const char* name, void (*kern)(KArgs...), dim3 grid, dim3 block,
-                                cudaStream_t stream, Args&&... args) {
+                                size_t smem, cudaStream_t stream, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

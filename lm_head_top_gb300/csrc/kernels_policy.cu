@@ -19,11 +19,10 @@
 // whose gradient pass reads the mask once more. On short batches it is the
 // launches: a batch that one block can hold takes one. In between it is chains of
 // dependent lookups, joins and starts, about 10 us a launch. On 8.4M tokens the
-// policy loss takes 42 us after a count of 9 (21 at the copy rate): 96
-// instructions a token at 2.0 of 4 a cycle, half of the stalls waits for loads.
-// Not the lever there: 128 or 256 tokens a piece, 16 to 40 warps an SM, runs by
-// block instead of by warp, the next piece prefetched to L2 or to registers,
-// arithmetic without branches; each measured within 10 %.
+// policy loss takes 38 us after a count of 9 (21 at the copy rate): about 96
+// instructions a token. Not the lever there: 128 or 256 tokens a piece, 16 to 40
+// warps an SM, runs by block instead of by warp, the next piece prefetched to L2
+// or to registers, arithmetic without branches; each measured within 10 %.
 #include <cuda_bf16.h>
 #include <math.h>
 #include <stdint.h>
@@ -42,6 +41,8 @@ constexpr int SEQ_WARPS = SEQ_THREADS / 32;
 constexpr int SEQ_TOK = 4;              // consecutive tokens per lane: a 16-byte load
 constexpr int SEQ_PIECE = 32 * SEQ_TOK;  // tokens of a warp's step
 constexpr int SEQ_RESIDENT = 2;          // blocks of a walk on an SM
+constexpr int RING_STAGES = 2;
+constexpr int RING_BYTES = 4 * SEQ_PIECE * 4 + SEQ_PIECE;  // a piece of four arrays and the mask
 constexpr int PREF_ONE_THREADS = 512;    // the one-block preference loss
 
 // First sequence in [lo, lo + n) whose end is past token t (the last one if
@@ -172,9 +173,29 @@ __device__ __forceinline__ Sum2 warp_sum(Sum2 v) {
 }
 
 // Tokens of one warp's run when `warps` of them share T tokens.
-__device__ __forceinline__ int run_length(int T, int warps) {
+__host__ __device__ __forceinline__ int run_length(int T, int warps) {
   return (int)(((long long)T + (long long)warps * SEQ_PIECE - 1) /
                ((long long)warps * SEQ_PIECE)) * SEQ_PIECE;
+}
+
+// Copies to shared memory that the thread waits for by groups.
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int LEFT>
+__device__ __forceinline__ void copy_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
 }
 
 // --------------------------------------------------------------- policy loss
@@ -271,7 +292,12 @@ __device__ __forceinline__ float exp_rest(float x) {
 // weighted sums of the two parts of the loss and the number of clipped tokens;
 // the block that finishes last joins the blocks' sums.
 //   NEED_SEQ: a token's sequence is looked up (advantages or weights per sequence).
-template <bool NEED_SEQ>
+//   RING: pieces come through shared memory, one ahead of the arithmetic, each
+//   lane copying what it will read itself (no barrier). For runs of several
+//   pieces and aligned arrays: loads waited for in registers were half of the
+//   stalls, and registers for the next piece do not fit beside this one's (the
+//   loss of 8.4M tokens 42 -> 38 us; two ahead the same).
+template <bool NEED_SEQ, bool RING>
 __global__ void __launch_bounds__(SEQ_THREADS, SEQ_RESIDENT)
     policy_loss_kernel(const PolicyArgs a, int* status) {
   __shared__ int count, any, clips;
@@ -289,7 +315,32 @@ __global__ void __launch_bounds__(SEQ_THREADS, SEQ_RESIDENT)
   const int begin = (int)min((long long)a.T, first);
   const int run_end = (int)min((long long)a.T, first + R);
 
-  if (lane < 8 && begin + lane * 32 < run_end) {  // two pieces are on their way during the lookups
+  extern __shared__ __align__(16) unsigned char ring_mem[];
+  const uint32_t ring = smem_u32(ring_mem) + warp * (RING_STAGES * RING_BYTES);
+  auto copy_ahead = [&](int t, int stage) {
+    if (t + SEQ_TOK <= run_end) {  // (a run ends at T or at a piece's end)
+      const uint32_t d = ring + stage * RING_BYTES + lane * 16;
+      copy_async16(d, a.logp + t);
+      if (a.old_logp) copy_async16(d + 512, a.old_logp + t);
+      if (a.ref_logp) copy_async16(d + 1024, a.ref_logp + t);
+      if (!a.adv_per_seq) copy_async16(d + 1536, a.advantages + t);
+      if (a.mask) copy_async4(ring + stage * RING_BYTES + 2048 + lane * 4, a.mask + t);
+    }
+    copy_async_commit();
+  };
+  auto read4 = [](uint32_t addr, float (&x)[SEQ_TOK]) {
+    const uint4 v = ld_shared_v4(addr);
+    x[0] = __uint_as_float(v.x);
+    x[1] = __uint_as_float(v.y);
+    x[2] = __uint_as_float(v.z);
+    x[3] = __uint_as_float(v.w);
+  };
+  int stage = 0;
+  // the first pieces are on their way during the lookups
+  if (RING) {
+    for (int k = 0; k < RING_STAGES - 1; ++k)
+      copy_ahead(begin + lane * SEQ_TOK + k * SEQ_PIECE, k);
+  } else if (lane < 8 && begin + lane * 32 < run_end) {
     prefetch_l2(a.logp + begin + lane * 32);
     if (a.old_logp) prefetch_l2(a.old_logp + begin + lane * 32);
     if (a.ref_logp) prefetch_l2(a.ref_logp + begin + lane * 32);
@@ -336,15 +387,33 @@ __global__ void __launch_bounds__(SEQ_THREADS, SEQ_RESIDENT)
   for (int p = begin; p < run_end; p += SEQ_PIECE) {
     const int t = p + lane * SEQ_TOK;
     if (t >= run_end) break;  // nothing below is collective
-    const uint32_t on = load_mask(a.mask, t, a.T, vec);
     const bool whole = vec && t + SEQ_TOK <= a.T;
+    uint32_t on;
     float lp[SEQ_TOK], lo[SEQ_TOK], lr[SEQ_TOK], adv[SEQ_TOK];
-    if (whole) {  // one test for all the loads
+    if (RING) {
+      const int last = stage == 0 ? RING_STAGES - 1 : stage - 1;
+      copy_ahead(t + (RING_STAGES - 1) * SEQ_PIECE, last);
+      copy_async_wait<RING_STAGES - 1>();
+    }
+    if (RING && whole) {
+      const uint32_t d = ring + stage * RING_BYTES + lane * 16;
+      read4(d, lp);
+      if (a.old_logp) read4(d + 512, lo);
+      if (a.ref_logp) read4(d + 1024, lr);
+      if (!a.adv_per_seq) read4(d + 1536, adv);
+      on = (1u << SEQ_TOK) - 1u;
+      if (a.mask)
+        on = nonzero_bytes(ld_shared_u32(ring + stage * RING_BYTES + 2048 + lane * 4));
+      stage = stage == RING_STAGES - 1 ? 0 : stage + 1;
+    } else {
+      on = load_mask(a.mask, t, a.T, vec);
+    }
+    if (whole && !RING) {  // one test for all the loads
       load_tok(a.logp, t, a.T, true, lp);
       if (a.old_logp) load_tok(a.old_logp, t, a.T, true, lo);
       if (a.ref_logp) load_tok(a.ref_logp, t, a.T, true, lr);
       if (!a.adv_per_seq) load_tok(a.advantages, t, a.T, true, adv);
-    } else {
+    } else if (!whole) {
       load_tok(a.logp, t, a.T, false, lp);
       if (a.old_logp) load_tok(a.old_logp, t, a.T, false, lo);
       if (a.ref_logp) load_tok(a.ref_logp, t, a.T, false, lr);
@@ -369,11 +438,10 @@ __global__ void __launch_bounds__(SEQ_THREADS, SEQ_RESIDENT)
       at = upto;
 #pragma unroll
       for (int j = 0; j < SEQ_TOK; ++j) {
-        // What lies under the mask is replaced before it is used: d = 0 is inside
-        // every border, and the advantage and the weight are zero.
+        // What lies under the mask is replaced before it is used: with d = x = A = 0
+        // a token is inside every border and adds nothing.
         const bool counts = (mine >> j) & 1u;
         const float A = counts ? (a.adv_per_seq ? w_adv : adv[j]) : 0.f;
-        const float wj = counts ? w : 0.f;
         const bool pos = A >= 0.f;
         float r = 1.f;
         bool clip = false;
@@ -391,16 +459,16 @@ __global__ void __launch_bounds__(SEQ_THREADS, SEQ_RESIDENT)
           }
         }
         const float rA = r * A;
-        pg1 = fmaf(-wj, rA, pg1);
+        pg1 = fmaf(-w, rA, pg1);
         float gj = clip ? 0.f : -rA;
         if (a.ref_logp) {
           const float x = counts ? lr[j] - lp[j] : 0.f;
           const float k = exp_rest(x);
-          kl1 = fmaf(wj, k, kl1);
+          kl1 = fmaf(w, k, kl1);
           gj = fmaf(-a.kl_coef, x + k, gj);
         }
         clipped += clip ? 1 : 0;
-        g[j] = fmaf(wj * a.grad_loss, gj, g[j]);
+        g[j] = fmaf(w * a.grad_loss, gj, g[j]);
       }
     } while (NEED_SEQ && at < min(t + SEQ_TOK, a.T));
     if (a.grad) {
@@ -701,15 +769,25 @@ cudaError_t launch_policy_loss(const PolicyArgs& a, int num_sms, int* status,
   const bool per_seq = a.reduction == 1;
   const dim3 block(SEQ_THREADS);
   const dim3 grid(policy_one_block(a.T, a.reduction) ? 1u : (unsigned)seq_blocks(a.T, num_sms));
-  const auto kernel = per_seq || a.adv_per_seq ? policy_loss_kernel<true> : policy_loss_kernel<false>;
+  const bool seq = per_seq || a.adv_per_seq;
+  const bool ring = a.vec && run_length(a.T, (int)grid.x * SEQ_WARPS) >= 4 * SEQ_PIECE;
+  const auto kernel = seq ? (ring ? policy_loss_kernel<true, true> : policy_loss_kernel<true, false>)
+                          : (ring ? policy_loss_kernel<false, true>
+                                  : policy_loss_kernel<false, false>);
+  const size_t smem = ring ? (size_t)SEQ_WARPS * RING_STAGES * RING_BYTES : 0;
+  if (ring) {  // (the same value every time: concurrent first calls do no harm)
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
   if (!per_seq && (!a.mask || a.count_here))
-    return launch_kernel("policy_loss", kernel, grid, block, 0, stream, a, status);
+    return launch_kernel("policy_loss", kernel, grid, block, smem, stream, a, status);
   // What the loss kernel reads before its wait was complete before the count began.
   const cudaError_t e =
       launch_kernel("policy_count", policy_count_kernel, grid, block, 0, stream, a.mask, a.cu, a.T,
                     a.S, a.vec, per_seq ? a.n_seq : nullptr, a.n_count);
   if (e != cudaSuccess) return e;
-  return launch_kernel_early("policy_loss", kernel, grid, block, stream, a, status);
+  return launch_kernel_early("policy_loss", kernel, grid, block, smem, stream, a, status);
 }
 
 cudaError_t launch_pref_loss(const PrefArgs& a, int num_sms, int* status, cudaStream_t stream) {
@@ -722,10 +800,10 @@ cudaError_t launch_pref_loss(const PrefArgs& a, int num_sms, int* status, cudaSt
       launch_kernel("pref_sums", pref_sums_kernel, grid, block, 0, stream, a, warps, status);
   if (e != cudaSuccess) return e;
   e = launch_kernel_early("pref_pairs", pref_pairs_kernel,
-                          dim3((unsigned)((a.P + SEQ_WARPS - 1) / SEQ_WARPS)), block, stream, a,
+                          dim3((unsigned)((a.P + SEQ_WARPS - 1) / SEQ_WARPS)), block, 0, stream, a,
                           warps, status);
   if (e != cudaSuccess) return e;
-  return launch_kernel_early("pref_grad", pref_grad_kernel, a.grad ? grid : dim3(1), block, stream,
+  return launch_kernel_early("pref_grad", pref_grad_kernel, a.grad ? grid : dim3(1), block, 0, stream,
                              a, warps);
 }
 

@@ -962,7 +962,7 @@ cudaError_t launch_f32_to_bf16(const float* in, uint16_t* out, long long n, int 
   const int blocks = std::max(1, std::min(T, num_sms * 8));
   if (early)
     return launch_kernel_early("f32_to_bf16", f32_to_bf16_kernel, dim3((unsigned)blocks), dim3(256),
-                               stream, reinterpret_cast<const float4*>(in),
+                               0, stream, reinterpret_cast<const float4*>(in),
                                reinterpret_cast<uint2*>(out), T, d / 4, invmap, parts, n / 4);
   return launch_kernel("f32_to_bf16", f32_to_bf16_kernel, dim3((unsigned)blocks), dim3(256), 0,
                        stream, reinterpret_cast<const float4*>(in), reinterpret_cast<uint2*>(out),
@@ -985,7 +985,7 @@ cudaError_t launch_token_rows(const uint16_t* H, const uint16_t* W, int d, const
   uint4* hc = reinterpret_cast<uint4*>(Hc);
   if (rowmap)  // the scan that wrote it is ahead; without one, nothing of this call's is
     return launch_kernel_early("token_rows", token_rows_kernel, dim3((unsigned)blocks), dim3(256),
-                               stream, h, w, d / 8, ids, rowmap, n_count, T, V, round, hc, sidx, sp,
+                               0, stream, h, w, d / 8, ids, rowmap, n_count, T, V, round, hc, sidx, sp,
                                zdot, status);
   return launch_kernel("token_rows", token_rows_kernel, dim3((unsigned)blocks), dim3(256), 0,
                        stream, h, w, d / 8, ids, rowmap, n_count, T, V, round, hc, sidx, sp, zdot,
@@ -998,10 +998,10 @@ cudaError_t launch_logp_combine(const float* pm, const float* ps, const float* p
   // Few tokens: more threads on each one's splits, and more blocks.
   if (T <= 4096)
     return launch_kernel_early("logp_combine", logp_combine_kernel<4>, dim3((T + 3) / 4),
-                               dim3(COMBINE_THREADS), stream, pm, ps, pd, nsplit, T, invmap,
+                               dim3(COMBINE_THREADS), 0, stream, pm, ps, pd, nsplit, T, invmap,
                          zdot, cl2, inv_tau, logp, lse);
   return launch_kernel_early("logp_combine", logp_combine_kernel<32>, dim3((T + 31) / 32),
-                             dim3(COMBINE_THREADS), stream, pm, ps, pd, nsplit, T, invmap,
+                             dim3(COMBINE_THREADS), 0, stream, pm, ps, pd, nsplit, T, invmap,
                        zdot, cl2, inv_tau, logp, lse);
 }
 

@@ -105,6 +105,44 @@ def test_policy_optional_inputs(kdkl, use_old, use_ref, use_mask, reduction):
         _policy_check(got, want, T)
 
 
+@pytest.mark.parametrize("T", [2_600_001, 2_600_003])
+@pytest.mark.parametrize("per_seq,reduction", [(True, "sequence"), (False, "token"), (False, "sum")])
+def test_policy_long_runs(kdkl, T, per_seq, reduction):
+    """Runs of several pieces per warp, through shared memory and (unaligned arrays)
+    without it: the same bits, and the definition in 64 bits by torch."""
+    S = 700
+    r, logp, old, ref, mask = _tokens(T, 7, True)
+    cu = _cu(T, S, r)
+    adv = r.normal(size=S if per_seq else T).astype(np.float32)
+    ins = [_cuda(x) for x in (logp, old, ref, adv, mask, cu)]
+    kw = dict(clip_low=0.2, clip_high=0.3, dual_clip=1.5, kl_coef=0.1, reduction=reduction,
+              norm=1e6, grad_loss=0.7)
+    got = kdkl.kd_policy_loss(*ins, **kw)
+    pad = torch.zeros(T + 1, device="cuda")
+    pad[1:] = ins[0]
+    plain = kdkl.kd_policy_loss(pad[1:], *ins[1:], **kw)
+    for a, b in zip(got, plain):
+        assert torch.equal(a, b)
+    on = ins[4] != 0
+    seq = torch.bucketize(torch.arange(T, device="cuda"), ins[5][1:].long(), right=True)
+    lp, lo, lr = (torch.where(on, t.double(), 0.0) for t in ins[:3])
+    A = ins[3].double()[seq] if per_seq else ins[3].double()
+    d, x = lp - lo, lr - lp
+    ratio = d.exp()
+    s = torch.minimum(ratio * A, ratio.clamp(0.8, 1.3) * A)
+    s = torch.where(A < 0, torch.maximum(s, 1.5 * A), s)
+    n = torch.zeros(S, dtype=torch.double, device="cuda").index_add_(0, seq, on.double())
+    w = {"token": on / on.sum().double(), "sum": on / 1e6,
+         "sequence": on / (n * (n > 0).sum()).clamp(min=1)[seq]}[reduction]
+    grad = 0.7 * w * (torch.where(s == ratio * A, -s, 0.0) - 0.1 * torch.expm1(x))
+    off = (got[2].double() - grad).abs()
+    assert (off <= 4 * U * torch.maximum(grad.abs(), grad.abs().mean())).all()
+    pg, kl = -(w * s).sum().item(), (w * (torch.expm1(x) - x)).sum().item()
+    size = (w * s.abs()).sum().item() + abs(kl)
+    assert abs(got[0].item() - pg - 0.1 * kl) <= U * size
+    assert abs(got[1][0].item() - pg) <= U * size and abs(got[1][1].item() - kl) <= U * size
+
+
 @pytest.mark.parametrize("reduction", ["token", "sequence"])
 def test_policy_many_empty_sequences(kdkl, reduction):
     """More sequences than tokens in a block, most of them empty."""
