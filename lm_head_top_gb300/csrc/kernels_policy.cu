@@ -224,6 +224,7 @@ __global__ void __launch_bounds__(SEQ_THREADS)
   };
   int total = 0;
   int s = 0, end = -1;
+  int held = 0, count = 0;  // a sequence's count not put yet
   if (n_seq && first < T) s = seq_find_warp(cu, 0, S, (int)first);
   for (int p = (int)min((long long)T, first); p < run_end; p += PIECE) {
     const int t = p + lane * TOK;
@@ -237,8 +238,14 @@ __global__ void __launch_bounds__(SEQ_THREADS)
     }
     const int s0 = __shfl_sync(0xffffffffu, s, 0);
     if (__all_sync(0xffffffffu, t >= run_end || (s == s0 && min(t + TOK, T) <= end))) {
-      const int all = __reduce_add_sync(0xffffffffu, c);
-      if (lane == 0) put(s0, all);
+      // the whole piece in one sequence: its count waits for the sequence's end
+      // (4 sequences of 2M tokens: 14 us with an atomic a piece, 8 so)
+      if (s0 != held) {
+        if (lane == 0) put(held, count);
+        held = s0;
+        count = 0;
+      }
+      count += __reduce_add_sync(0xffffffffu, c);
     } else if (t < run_end) {
       int at = 0;  // the lane's tokens from here on are not put yet
       while (end < t + TOK && s < S - 1) {
@@ -252,6 +259,7 @@ __global__ void __launch_bounds__(SEQ_THREADS)
       put(s, __popc(on & ~((1u << at) - 1u)));
     }
   }
+  if (n_seq && lane == 0) put(held, count);
   total = __reduce_add_sync(0xffffffffu, total);
   if (lane == 0 && total) atomicAdd(&block_count, total);
   __syncthreads();
