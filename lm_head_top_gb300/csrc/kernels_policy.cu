@@ -19,7 +19,7 @@
 // whose gradient pass reads the mask once more. On short batches it is the
 // launches: a batch that one block can hold takes one. In between it is chains of
 // dependent lookups, joins and starts, about 10 us a launch. On 8.4M tokens the
-// policy loss takes 38 us after a count of 9 (21 at the copy rate): about 90
+// policy loss takes 38 us after a count of 9 (21 at the copy rate): about 95
 // instructions a token. Not the lever there: 128 or 256 tokens a piece, 16 to 40
 // warps an SM, runs by block instead of by warp, the next piece prefetched to L2
 // or to registers, arithmetic without branches; each measured within 10 %.

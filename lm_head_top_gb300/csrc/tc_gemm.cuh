@@ -105,8 +105,9 @@ struct GemmShape {
   // When > 0 (with first_group): split 0 covers n-tiles [0, first_ntiles)
   // and splits 1.. share the rest evenly; 0: every split gets an even share.
   int first_ntiles;
-  // Unit counter for this launch (zero before it starts): the leader CTA's
-  // producer takes the next unit with atomicAdd. nullptr: static round-robin
+  // Unit counter for this launch (zero before it starts): after its first unit
+  // (its group's number) the leader CTA's producer takes the next one with
+  // atomicAdd. nullptr: static round-robin
   // (CTA group g takes units g, g + groups, ...), kept to compare schedules.
   int* counter;
   // Token rows counted on the device (masked tokens compacted away): when
@@ -494,7 +495,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
   auto release_unit = [&](int q) {
     const int slot = q & (NSLOT - 1);
     if (PAIR)
-      mbar_arrive_cluster(uempty_leader0 + 8u * slot);
+      mbar_arrive_cluster_read(uempty_leader0 + 8u * slot);
     else
       mbar_arrive(uempty_bar(slot));
   };
@@ -512,38 +513,48 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
       long long fills = 0;
       bool ok = sh.inject_stall == 0;
       const uint32_t full_leader0 = PAIR ? mapa_shared(full_bar(0), 0) : full_bar(0);
-      // The leader's producer is also the scheduler: it takes units from the
-      // launch's counter (the next one fetched a unit ahead, so the atomic's
-      // latency hides behind a unit of copies) and publishes each in the ring.
+      // The leader's producer is also the scheduler. Its first unit is its
+      // group's number, the others come from the launch's counter. A unit's
+      // successor is asked for when its copies begin and published after the
+      // first of them: the atomic's latency hides behind copies, and the peer's
+      // producer, which is told through shared memory of another SM, goes on
+      // from unit to unit without a gap.
       const bool dyn = sh.counter != nullptr;
-      int next = (ok && leader) ? (dyn ? atomicAdd(sh.counter, 1) : group0) : -1;
       const uint32_t peer_slot0 = PAIR ? mapa_shared(smem_u32((const void*)unit_slot), 1) : 0u;
       const uint32_t peer_ufull0 = PAIR ? mapa_shared(ufull_bar(0), 1) : 0u;
+      auto publish = [&](int uq, int u) -> bool {
+        const int slot = uq & (NSLOT - 1);
+        const uint32_t ph = ((uint32_t)(uq / NSLOT) & 1u) ^ 1u;
+        const bool freed =
+            PAIR ? mbar_wait_cluster_bounded(uempty_bar(slot), ph, abort_flag, status, limit)
+                 : mbar_wait_bounded(uempty_bar(slot), ph, abort_flag, status, limit);
+        if (!freed) return false;
+        unit_slot[slot] = u;
+        if (PAIR)
+          st_async_cluster_u32(peer_slot0 + 4u * slot, (uint32_t)u, peer_ufull0 + 8u * slot);
+        mbar_arrive(ufull_bar(slot));
+        return true;
+      };
+      // the peer's slots: each filling is one 4-byte store that counts itself
+      if (PAIR && !leader)
+        for (int i = 0; i < NSLOT; ++i) mbar_arrive_expect_tx(ufull_bar(i), 4);
+      int next = group0 < units_all ? group0 : -1;
+      if (ok && leader) ok = publish(0, next);
       for (int uq = 0; ok; ++uq) {
         int u = -1;
+        bool owed = false;  // the successor is not published yet
         if (leader) {
-          const int slot = uq & (NSLOT - 1);
-          const uint32_t ph = ((uint32_t)(uq / NSLOT) & 1u) ^ 1u;
-          const bool freed =
-              PAIR ? mbar_wait_cluster_bounded(uempty_bar(slot), ph, abort_flag, status, limit)
-                   : mbar_wait_bounded(uempty_bar(slot), ph, abort_flag, status, limit);
-          if (!freed) {
-            ok = false;
-            break;
+          u = next;
+          if (u >= 0) {
+            next = dyn ? groups + atomicAdd(sh.counter, 1) : u + groups;
+            owed = true;
           }
-          u = next < units_all ? next : -1;
-          if (u >= 0) next = dyn ? atomicAdd(sh.counter, 1) : next + groups;
-          unit_slot[slot] = u;
-          if (PAIR) {
-            st_shared_cluster_u32(peer_slot0 + 4u * slot, (uint32_t)u);
-            mbar_arrive_cluster(peer_ufull0 + 8u * slot);
-          }
-          mbar_arrive(ufull_bar(slot));
         } else {
           if (!take_unit(uq, u)) {
             ok = false;
             break;
           }
+          if (PAIR) mbar_arrive_expect_tx(ufull_bar(uq & (NSLOT - 1)), 4);  // its next filling
           release_unit(uq);
         }
         if (u < 0) break;
@@ -597,7 +608,19 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
               stage = 0;
               phase ^= 1u;
             }
+            if (owed) {
+              owed = false;
+              if (next >= units_all) next = -1;
+              if (!publish(uq + 1, next)) {
+                ok = false;
+                break;
+              }
+            }
           }
+        }
+        if (ok && owed) {  // a unit without K steps
+          if (next >= units_all) next = -1;
+          ok = publish(uq + 1, next);
         }
       }
       // Teardown: every copy issued must have landed before the CTA exits. The

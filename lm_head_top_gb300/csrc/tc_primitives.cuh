@@ -275,9 +275,22 @@ __device__ __forceinline__ void mbar_arrive_cluster_tmem(uint32_t cluster_addr) 
                : "memory");
 }
 
-// 32-bit store into shared memory of a CTA of this cluster (mapa address).
-__device__ __forceinline__ void st_shared_cluster_u32(uint32_t cluster_addr, uint32_t v) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+// The same instruction for a barrier that hands back a slot of this CTA's shared
+// memory which was only read: the read is over, and nothing this thread wrote
+// has to be seen by the one that fills the slot again.
+__device__ __forceinline__ void mbar_arrive_cluster_read(uint32_t cluster_addr) {
+  mbar_arrive_cluster_tmem(cluster_addr);
+}
+
+// 32-bit store into shared memory of a CTA of this cluster (mapa addresses) that
+// counts 4 bytes on an mbarrier there when it lands: no fence between a store
+// and an arrival, which would wait for everything the thread has outstanding.
+__device__ __forceinline__ void st_async_cluster_u32(uint32_t cluster_addr, uint32_t v,
+                                                     uint32_t cluster_bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(
+                   cluster_addr),
+               "r"(v), "r"(cluster_bar)
+               : "memory");
 }
 
 // try_wait with acquire at cluster scope (pairs with mbar_arrive_cluster).
