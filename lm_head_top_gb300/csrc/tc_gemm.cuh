@@ -13,8 +13,9 @@
 //             admission threshold, compacted to the row's top-K per split.
 //   EPI_LSE_MIX / EPI_GRAD_MIX  the soft KL mixed with a hard-label CE.
 //
-// Roles per CTA (192 threads): warp 0 = TMA producer, warp 1 = MMA issuer and
-// TMEM owner, warps 2..5 = epilogue (warp w reads TMEM lanes 32*(w%4)..+31).
+// Roles per CTA (224 threads): warp 0 = TMA producer, warp 1 = MMA issuer and
+// TMEM owner, warps 2..5 = epilogue (warp w reads TMEM lanes 32*(w%4)..+31),
+// warp 6 = scheduler, which takes units and hands them to the other roles.
 // By default two CTAs of a cluster share a 256 x 256 tile (tcgen05
 // cta_group::2; PAIR); otherwise tiles are 128 x BN. The K step is 64 deep,
 // with as many shared-memory stages as fit in ~200 KB (6 for pairs), and two
@@ -38,7 +39,8 @@ namespace kdkl {
 constexpr int BM = 128;
 constexpr int BK = 64;
 constexpr int A_STAGE_BYTES = BM * BK * 2;
-constexpr int GEMM_THREADS = 192;
+// Warp 0: copies; 1: MMAs; 2 to 5: epilogue; 6: units.
+constexpr int GEMM_THREADS = 224;
 constexpr uint32_t TMEM_COLS = 512;  // two accumulators of up to 256 fp32 columns
 // MN-major operands arrive as 64-element-wide atoms of BK rows each.
 constexpr uint32_t MN_ATOM_BYTES = BK * 128;
@@ -52,6 +54,10 @@ constexpr int LOGIT_BN = 256;
 // the warp writes whole 128-byte row pieces: 32 line accesses.
 constexpr int EPI_WARP_BYTES = 32 * 128;
 
+// Ring of units handed from the scheduler to every other role.
+constexpr int UNIT_SLOTS = 4;
+constexpr int UNIT_BYTES = 32;  // Unit
+
 // Shared-memory plan for an MMA tile of TILE_M x BN. With PAIR, two CTAs of a
 // cluster share one 256 x BN tile: each holds 128 rows of A and BN/2 rows of B
 // (so half the B bytes per CTA) and its own 128 x BN accumulator. As many
@@ -64,10 +70,11 @@ struct TileCfg {
   static constexpr int B_STAGE_BYTES = B_ROWS * BK * 2;
   static constexpr int STAGE_BYTES = A_STAGE_BYTES + B_STAGE_BYTES;
   static constexpr int STAGES = (200 * 1024) / STAGE_BYTES > 8 ? 8 : (200 * 1024) / STAGE_BYTES;
-  // full, empty, tmem full x2, tmem empty x2, drain, unit-slot full / empty
-  static constexpr int NUM_BARS = 2 * STAGES + 5 + 2 * 4;
-  static constexpr int BAR_BYTES = 512;  // barriers, the unit ring, flags
-  static_assert(NUM_BARS * 8 + 64 <= BAR_BYTES, "barrier region");
+  // full, empty, tmem full x2, tmem empty x2, drain, unit-slot full / empty, begun
+  static constexpr int NUM_BARS = 2 * STAGES + 5 + 2 * UNIT_SLOTS + 1;
+  static constexpr int BAR_BYTES = 512;  // barriers, flags, the unit ring
+  static constexpr int UNIT_BYTES_AT = BAR_BYTES - UNIT_SLOTS * UNIT_BYTES;
+  static_assert(NUM_BARS * 8 + 16 <= UNIT_BYTES_AT, "barrier region");
   static constexpr int SMEM_BYTES =
       STAGES * STAGE_BYTES + 1024 /*alignment slack*/ + BAR_BYTES + 4 * EPI_WARP_BYTES;
 };
@@ -106,7 +113,7 @@ struct GemmShape {
   // and splits 1.. share the rest evenly; 0: every split gets an even share.
   int first_ntiles;
   // Unit counter for this launch (zero before it starts): after its first unit
-  // (its group's number) the leader CTA's producer takes the next one with
+  // (its group's number) the leader CTA's scheduler takes the next one with
   // atomicAdd. nullptr: static round-robin
   // (CTA group g takes units g, g + groups, ...), kept to compare schedules.
   int* counter;
@@ -336,6 +343,13 @@ __device__ __forceinline__ void unit_coords(const GemmShape& sh, int u, int& m, 
   split_range(sh, s, nb, ne);
 }
 
+// A unit as its roles need it: tiles (m, nb .. ne - 1) of split s, K steps
+// [kb, ke) of part `part`, of job `job` (see DUAL). m < 0: no more units.
+struct Unit {
+  int m, s, nb, ne, kb, ke, part, job;
+};
+static_assert(sizeof(Unit) == UNIT_BYTES, "two 16-byte pieces");
+
 // First position in the sorted id row whose id is >= v (K when none).
 __device__ __forceinline__ int lower_bound_row(const int32_t* row, int K, int v) {
   int lo = 0, hi = K;
@@ -391,10 +405,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE_BYTES);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NUM_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  // Ring of units handed from the scheduler (the leader CTA's producer) to
-  // every other role of both CTAs: slot i holds a unit number (-1: no more).
-  constexpr int NSLOT = 4;
-  volatile int* unit_slot = reinterpret_cast<volatile int*>(tmem_slot + 2);
+  constexpr int NSLOT = UNIT_SLOTS;
 
   const uint32_t bar0 = smem_u32(bars);
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
@@ -404,6 +415,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
   const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 4);
   auto ufull_bar = [&](int i) { return bar0 + 8u * (2 * STAGES + 5 + i); };
   auto uempty_bar = [&](int i) { return bar0 + 8u * (2 * STAGES + 5 + NSLOT + i); };
+  const uint32_t begun_bar = bar0 + 8u * (2 * STAGES + 5 + 2 * NSLOT);
+  auto unit_slot = [&](int i) { return bar0 + Cfg::UNIT_BYTES_AT + UNIT_BYTES * i; };
 
   grid_dependents_go();
   const int warp = threadIdx.x >> 5;
@@ -425,13 +438,14 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
       mbar_init(tempty_bar(b), PAIR ? 8 : 4);
     }
     mbar_init(drain_bar, 1);
-    // A slot is released by every role that reads it: the MMA thread and the
-    // 4 epilogue warps here, and with a pair the peer's producer and its 4
-    // epilogue warps (remote arrives on the leader's barrier).
+    // A slot is released by every role that reads it: the producer, the MMA
+    // thread and the 4 epilogue warps here, and with a pair the peer's producer
+    // and its 4 epilogue warps (remote arrives on the leader's barrier).
     for (int i = 0; i < NSLOT; ++i) {
       mbar_init(ufull_bar(i), 1);
-      mbar_init(uempty_bar(i), PAIR ? 10 : 5);
+      mbar_init(uempty_bar(i), PAIR ? 11 : 6);
     }
+    mbar_init(begun_bar, 1);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmA);
@@ -471,11 +485,10 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
   }
   const int units0 = sh.units;
   const int units_all = units0 + (DUAL ? sh1.units : 0);
-  // Per unit: its job's shape, the unit within that job, and A's layout.
-  auto job_of = [&](int u, const GemmShape*& js, int& uu, bool& a_mn) {
-    const bool j1 = DUAL && u >= units0;
+  // Per unit: its job's shape, and A's layout.
+  auto job_of = [&](const Unit& u, const GemmShape*& js, bool& a_mn) {
+    const bool j1 = DUAL && u.job != 0;
     js = j1 ? &sh1 : &sh;
-    uu = j1 ? u - units0 : u;
     a_mn = j1 ? !A_MN : A_MN;
     return j1;
   };
@@ -484,13 +497,15 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
   // acquire with a pair: the leader wrote the peer's slot remotely), then
   // release the slot on the leader's barrier once the value is read.
   const uint32_t uempty_leader0 = PAIR ? mapa_shared(uempty_bar(0), 0) : uempty_bar(0);
-  auto take_unit = [&](int q, int& u) -> bool {
+  auto take_unit = [&](int q, Unit& u) -> bool {
     const int slot = q & (NSLOT - 1);
     const uint32_t ph = (uint32_t)(q / NSLOT) & 1u;
     const bool got = PAIR ? mbar_wait_cluster_bounded(ufull_bar(slot), ph, abort_flag, status, limit)
                           : mbar_wait_bounded(ufull_bar(slot), ph, abort_flag, status, limit);
-    if (got) u = unit_slot[slot];
-    return got;
+    if (!got) return false;
+    const uint4 a = ld_shared_v4(unit_slot(slot)), b = ld_shared_v4(unit_slot(slot) + 16);
+    u = Unit{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
+    return true;
   };
   auto release_unit = [&](int q) {
     const int slot = q & (NSLOT - 1);
@@ -513,68 +528,33 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
       long long fills = 0;
       bool ok = sh.inject_stall == 0;
       const uint32_t full_leader0 = PAIR ? mapa_shared(full_bar(0), 0) : full_bar(0);
-      // The leader's producer is also the scheduler. Its first unit is its
-      // group's number, the others come from the launch's counter. A unit's
-      // successor is asked for when its copies begin and published after the
-      // first of them: the atomic's latency hides behind copies, and the peer's
-      // producer, which is told through shared memory of another SM, goes on
-      // from unit to unit without a gap.
-      const bool dyn = sh.counter != nullptr;
-      const uint32_t peer_slot0 = PAIR ? mapa_shared(smem_u32((const void*)unit_slot), 1) : 0u;
-      const uint32_t peer_ufull0 = PAIR ? mapa_shared(ufull_bar(0), 1) : 0u;
-      auto publish = [&](int uq, int u) -> bool {
-        const int slot = uq & (NSLOT - 1);
-        const uint32_t ph = ((uint32_t)(uq / NSLOT) & 1u) ^ 1u;
-        const bool freed =
-            PAIR ? mbar_wait_cluster_bounded(uempty_bar(slot), ph, abort_flag, status, limit)
-                 : mbar_wait_bounded(uempty_bar(slot), ph, abort_flag, status, limit);
-        if (!freed) return false;
-        unit_slot[slot] = u;
-        if (PAIR)
-          st_async_cluster_u32(peer_slot0 + 4u * slot, (uint32_t)u, peer_ufull0 + 8u * slot);
-        mbar_arrive(ufull_bar(slot));
-        return true;
-      };
-      // the peer's slots: each filling is one 4-byte store that counts itself
+      // the peer's slots: a filling is two stores that count themselves
       if (PAIR && !leader)
-        for (int i = 0; i < NSLOT; ++i) mbar_arrive_expect_tx(ufull_bar(i), 4);
-      int next = group0 < units_all ? group0 : -1;
-      if (ok && leader) ok = publish(0, next);
+        for (int i = 0; i < NSLOT; ++i) mbar_arrive_expect_tx(ufull_bar(i), UNIT_BYTES);
       for (int uq = 0; ok; ++uq) {
-        int u = -1;
-        bool owed = false;  // the successor is not published yet
-        if (leader) {
-          u = next;
-          if (u >= 0) {
-            next = dyn ? groups + atomicAdd(sh.counter, 1) : u + groups;
-            owed = true;
-          }
-        } else {
-          if (!take_unit(uq, u)) {
-            ok = false;
-            break;
-          }
-          if (PAIR) mbar_arrive_expect_tx(ufull_bar(uq & (NSLOT - 1)), 4);  // its next filling
-          release_unit(uq);
+        Unit u;
+        if (!take_unit(uq, u)) {
+          ok = false;
+          break;
         }
-        if (u < 0) break;
+        if (leader)
+          mbar_arrive(begun_bar);
+        else
+          mbar_arrive_expect_tx(ufull_bar(uq & (NSLOT - 1)), UNIT_BYTES);  // its next filling
+        release_unit(uq);
+        if (u.m < 0) break;
         const GemmShape* js;
-        int uu;
         bool a_mn;
-        const bool j1 = job_of(u, js, uu, a_mn);
+        const bool j1 = job_of(u, js, a_mn);
         const CUtensorMap* ta = j1 ? &tmA1 : &tmA;
         const CUtensorMap* tb = j1 ? &tmB1 : &tmB;
-        int kb0 = 0, kb1 = js->k_blocks;
-        if (EPI == EPI_STORE) unit_k_part(*js, uu, kb0, kb1);
-        int m, s, nb, ne;
-        unit_coords(*js, uu, m, s, nb, ne);
-        const int a_row = js->a_m0 + m * TILE_M + (int)rank * BM;
-        for (int n = nb; ok && n < ne; ++n) {
+        const int a_row = js->a_m0 + u.m * TILE_M + (int)rank * BM;
+        for (int n = u.nb; ok && n < u.ne; ++n) {
           const bool narrow = B_MN && js->narrow_last && n == js->n_tiles - 1;
           const int b_rows = narrow ? B_ROWS / 2 : B_ROWS;  // B rows this CTA copies
           const int b_row = js->b_n0 + n * BN + (int)rank * b_rows;
           const uint32_t stage_bytes = (uint32_t)(A_STAGE_BYTES + b_rows * BK * 2);
-          for (int kb = kb0; kb < kb1; ++kb) {
+          for (int kb = u.kb; kb < u.ke; ++kb) {
             if (!mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, status, limit)) {
               ok = false;
               break;
@@ -608,19 +588,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
               stage = 0;
               phase ^= 1u;
             }
-            if (owed) {
-              owed = false;
-              if (next >= units_all) next = -1;
-              if (!publish(uq + 1, next)) {
-                ok = false;
-                break;
-              }
-            }
           }
-        }
-        if (ok && owed) {  // a unit without K steps
-          if (next >= units_all) next = -1;
-          ok = publish(uq + 1, next);
         }
       }
       // Teardown: every copy issued must have landed before the CTA exits. The
@@ -643,23 +611,18 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
       uint32_t acc_phase = 0;
       bool ok = true;
       for (int uq = 0; ok; ++uq) {
-        int u = -1;
+        Unit u;
         if (!take_unit(uq, u)) break;
         release_unit(uq);
-        if (u < 0) break;
+        if (u.m < 0) break;
         const GemmShape* js;
-        int uu;
         bool a_mn;
-        const bool j1 = job_of(u, js, uu, a_mn);
+        const bool j1 = job_of(u, js, a_mn);
         // No K steps (no counted token in a dW launch): nothing to multiply;
         // the epilogue writes zeros without touching TMEM.
         if (js->k_blocks == 0) continue;
         const uint32_t idesc = j1 ? idesc1 : idesc0;
-        int kb0 = 0, kb1 = js->k_blocks;
-        if (EPI == EPI_STORE) unit_k_part(*js, uu, kb0, kb1);
-        int m, s, nb, ne;
-        unit_coords(*js, uu, m, s, nb, ne);
-        for (int n = nb; ok && n < ne; ++n) {
+        for (int n = u.nb; ok && n < u.ne; ++n) {
           // the narrow last tile (see GemmShape::narrow_last) multiplies N = BN/2
           const bool narrow = B_MN && js->narrow_last && n == js->n_tiles - 1;
           const uint32_t idesc_n =
@@ -674,7 +637,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
           }
           tc_fence_after();
           const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
-          for (int kb = kb0; kb < kb1; ++kb) {
+          for (int kb = u.kb; kb < u.ke; ++kb) {
             if (!mbar_wait_bounded(full_bar(stage), phase, abort_flag, status, limit)) {
               ok = false;
               break;
@@ -689,9 +652,9 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
               const uint64_t bd = B_MN ? sdesc_sw128(b_base + k * 2048, MN_ATOM_BYTES, 1024)
                                        : sdesc_sw128(b_base + k * 32, 16, 1024);
               if (PAIR)
-                tc_mma_bf16_pair(d_tmem, ad, bd, idesc_n, (kb != kb0 || k != 0) ? 1u : 0u);
+                tc_mma_bf16_pair(d_tmem, ad, bd, idesc_n, (kb != u.kb || k != 0) ? 1u : 0u);
               else
-                tc_mma_bf16(d_tmem, ad, bd, idesc_n, (kb != kb0 || k != 0) ? 1u : 0u);
+                tc_mma_bf16(d_tmem, ad, bd, idesc_n, (kb != u.kb || k != 0) ? 1u : 0u);
             }
             if (PAIR)
               tc_commit_pair_multicast(empty_bar(stage), 0x3);
@@ -717,6 +680,56 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
       else
         tc_commit(drain_bar);
       mbar_drain_bounded(drain_bar, 0);
+    }
+  } else if (warp == 6) {
+    if (lane == 0 && leader && sh.inject_stall == 0) {
+      // -------------------------------------------------------- scheduler
+      // The first unit is the group's number, the others come from the launch's
+      // counter: asked for, taken apart (four or more divisions, some of 64 bits:
+      // about 0.7 us, as long as two K steps) and handed to the roles of both CTAs
+      // while the unit before it is copied.
+      const bool dyn = sh.counter != nullptr;
+      const uint32_t peer_slots = PAIR ? mapa_shared(unit_slot(0), 1) : 0u;
+      const uint32_t peer_ufull0 = PAIR ? mapa_shared(ufull_bar(0), 1) : 0u;
+      int next = group0;
+      bool ended = false;
+      for (int uq = 0; !ended; ++uq) {
+        if (uq > 0) {
+          // not before the copies of the unit before: units go to who is ready
+          if (!mbar_wait_bounded(begun_bar, (uint32_t)(uq - 1) & 1u, abort_flag, status, limit))
+            break;
+          next = dyn ? groups + atomicAdd(sh.counter, 1) : next + groups;
+        }
+        Unit u = {-1, 0, 0, 0, 0, 0, 0, 0};
+        if (next < units_all) {
+          u.job = DUAL && next >= units0 ? 1 : 0;
+          const GemmShape& js = u.job ? sh1 : sh;
+          int uu = u.job ? next - units0 : next;
+          u.ke = js.k_blocks;
+          if (EPI == EPI_STORE) u.part = unit_k_part(js, uu, u.kb, u.ke);
+          unit_coords(js, uu, u.m, u.s, u.nb, u.ne);
+        }
+        const int slot = uq & (NSLOT - 1);
+        const uint32_t ph = ((uint32_t)(uq / NSLOT) & 1u) ^ 1u;
+        const bool freed =
+            PAIR ? mbar_wait_cluster_bounded(uempty_bar(slot), ph, abort_flag, status, limit)
+                 : mbar_wait_bounded(uempty_bar(slot), ph, abort_flag, status, limit);
+        if (!freed) break;
+        const uint4 a = make_uint4(u.m, u.s, u.nb, u.ne), b = make_uint4(u.kb, u.ke, u.part, u.job);
+        if (PAIR) {
+          const uint32_t d = peer_slots + UNIT_BYTES * slot, bar = peer_ufull0 + 8u * slot;
+          st_async_cluster_v4(d, a, bar);
+          st_async_cluster_v4(d + 16, b, bar);
+        }
+        st_shared_v4(unit_slot(slot), a);
+        st_shared_v4(unit_slot(slot) + 16, b);
+        mbar_arrive(ufull_bar(slot));
+        ended = u.m < 0;
+      }
+      // Given up: the peer may not wait for the last unit's stores, so they land
+      // first (20 us are many times their way).
+      if (PAIR && !ended)
+        for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 20000;) {}
     }
   } else {
     // --------------------------------------------------------------- epilogue
@@ -814,7 +827,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
       if (lane == 0) ep.unit_cnt[(long long)pend_s * ep.T + row] = w;
     };
     for (int uq = 0; ok; ++uq) {  // uq: position in the unit ring (q is the lane quarter)
-      int u = -1;
+      Unit u;
       const bool got_unit = __all_sync(0xffffffffu, take_unit(uq, u));
       if (!got_unit) {
         ok = false;
@@ -822,17 +835,13 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
       }
       __syncwarp();  // every lane has read the slot before it is released
       if (lane == 0) release_unit(uq);
-      if (u < 0) break;
+      if (u.m < 0) break;
       const GemmShape* js;
-      int uu;
       bool a_mn_unused;
-      const bool j1 = job_of(u, js, uu, a_mn_unused);
+      const bool j1 = job_of(u, js, a_mn_unused);
       const EpiParams& eo = j1 ? ep1 : ep;  // the unit's output (store epilogues)
       const bool no_k = js->k_blocks == 0;  // zeros, no TMEM (see the MMA role)
-      int k_part = 0, kb_unused, ke_unused;
-      if (EPI == EPI_STORE) k_part = unit_k_part(*js, uu, kb_unused, ke_unused);
-      int m, s, nb, ne;
-      unit_coords(*js, uu, m, s, nb, ne);
+      const int k_part = u.part, m = u.m, s = u.s, nb = u.nb, ne = u.ne;
       const int r = m * TILE_M + (int)rank * BM + r_in_tile;  // row within this launch
       // per-unit row state
       float run_max = -INFINITY, run_sum = 0.f, dot = 0.f;

@@ -282,15 +282,16 @@ __device__ __forceinline__ void mbar_arrive_cluster_read(uint32_t cluster_addr) 
   mbar_arrive_cluster_tmem(cluster_addr);
 }
 
-// 32-bit store into shared memory of a CTA of this cluster (mapa addresses) that
-// counts 4 bytes on an mbarrier there when it lands: no fence between a store
+// 16-byte store into shared memory of a CTA of this cluster (mapa addresses) that
+// counts its bytes on an mbarrier there when it lands: no fence between a store
 // and an arrival, which would wait for everything the thread has outstanding.
-__device__ __forceinline__ void st_async_cluster_u32(uint32_t cluster_addr, uint32_t v,
-                                                     uint32_t cluster_bar) {
-  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(
-                   cluster_addr),
-               "r"(v), "r"(cluster_bar)
-               : "memory");
+__device__ __forceinline__ void st_async_cluster_v4(uint32_t cluster_addr, uint4 v,
+                                                    uint32_t cluster_bar) {
+  asm volatile(
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::
+          "r"(cluster_addr),
+      "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"(cluster_bar)
+      : "memory");
 }
 
 // try_wait with acquire at cluster scope (pairs with mbar_arrive_cluster).
