@@ -210,12 +210,19 @@ bool static_schedule() {
 // the backward workspaces (from `base` on), so that a backward can read the
 // forward's: sorted ids and p [T, K]; when a mask is given, the compaction of
 // the counted tokens: rowmap [T] (row -> token), invmap [T] (token -> row or
-// -1) and Hc, H's counted rows [T_pad, d] bf16 (T_pad = T rounded up to 256).
+// -1) and Hc, H's counted rows [T_pad, hc_ld] bf16 (T_pad = T rounded up to 256;
+// hc_ld = d but for the calls on token log-probabilities, see line_ld).
 struct TeacherLayout {
   size_t off_sidx, off_sp, off_rowmap, off_invmap, off_Hc, end;
 };
 
-TeacherLayout teacher_layout(size_t base, const kd_kl_problem& p) {
+// Row length of a copy whose rows start on 128-byte lines. A K step's 128 bytes
+// of a row off them touch two lines, and every row is read by as many CTA pairs as
+// there are vocabulary tiles: at d = 1000, V = 32,003 the forward's product of 639
+// tokens took 49 us and takes 44, of 4096 the backward's first 202 and 171.
+int64_t line_ld(int64_t d) { return round_up(d, 64); }
+
+TeacherLayout teacher_layout(size_t base, const kd_kl_problem& p, int64_t hc_ld) {
   TeacherLayout L{};
   const size_t TK = (size_t)p.T * p.K;
   size_t o = base;
@@ -223,7 +230,7 @@ TeacherLayout teacher_layout(size_t base, const kd_kl_problem& p) {
   L.off_sp = o; o = align256(o + TK * 4);
   L.off_rowmap = o; o = align256(o + (size_t)p.T * 4);
   L.off_invmap = o; o = align256(o + (size_t)p.T * 4);
-  L.off_Hc = o; o = align256(o + (size_t)round_up(p.T, 2 * BM) * p.d * 2);
+  L.off_Hc = o; o = align256(o + (size_t)round_up(p.T, 2 * BM) * hc_ld * 2);
   L.end = o;
   return L;
 }
@@ -249,6 +256,7 @@ struct BwdPlan {
   // (none when the backward reads the forward's)
   size_t off_ctr;
   TeacherLayout tl;
+  int64_t hc_ld;
   int dH_parts;  // dH is summed in so many parts of a block's vocabulary
   size_t off_G, off_dH, total;
 };
@@ -264,9 +272,9 @@ bool problem_ok(const kd_kl_problem* p) {
   return true;
 }
 
-// split_tiles: vocabulary tiles per unit, 0 = the default.
-FwdPlan plan_forward(const kd_kl_problem& p, int num_sms, bool pair, int procs, bool mix = false,
-                     int split_tiles = 0) {
+// split_tiles: vocabulary tiles per unit, 0 = the default. hc_ld: see TeacherLayout.
+FwdPlan plan_forward(const kd_kl_problem& p, int num_sms, bool pair, int procs, bool mix,
+                     int split_tiles, int64_t hc_ld) {
   (void)num_sms;
   FwdPlan f{};
   const int tile_m = pair ? 2 * BM : BM;
@@ -278,7 +286,7 @@ FwdPlan plan_forward(const kd_kl_problem& p, int num_sms, bool pair, int procs, 
   f.nsplit = p.T > 0 ? lp.nsplit : 1;
   f.group_m = lp.group_m;
   f.grid = (pair ? 2 : 1) * (int)std::min<int64_t>((int64_t)f.m_tiles * f.nsplit, procs);
-  f.tl = teacher_layout(kHeaderBytes, p);
+  f.tl = teacher_layout(kHeaderBytes, p, hc_ld);
   size_t o = f.tl.end;
   f.off_ent = o; o = align256(o + (size_t)p.T * 4);
   f.off_pm = o; o = align256(o + (size_t)f.nsplit * p.T * 4);
@@ -373,9 +381,10 @@ int dH_split(int64_t T, int64_t d, int64_t Vb) {
 // sp in its workspace); otherwise it reads the forward's.
 // whole_dW: every dW tile comes from one launch (all tokens per vocabulary
 // slab, however many there are), as a dW rounded to bf16 on its way out needs.
-// split_dH: the dH products may be cut along the vocabulary (see dH_split).
+// per_token (gradients): the dH products may be cut along the vocabulary (see
+// dH_split), and Hc's rows start on lines (see line_ld).
 BwdPlan plan_backward(const kd_kl_problem& p, bool own_teacher = true, bool whole_dW = false,
-                      bool split_dH = false) {
+                      bool per_token = false) {
   BwdPlan b{};
   const int64_t T = std::max<int64_t>(p.T, 1);
   const double budget = (double)p.chunk * (double)p.V;  // gradient-of-logits elements
@@ -393,10 +402,11 @@ BwdPlan plan_backward(const kd_kl_problem& p, bool own_teacher = true, bool whol
   b.Vb_pad = round_up(b.Vb, LOGIT_BN);
   size_t o = kHeaderBytes;
   b.off_ctr = o; o = align256(o + (size_t)3 * b.n_tblocks * b.n_vblocks * 4);
-  b.tl = teacher_layout(o, p);
+  b.hc_ld = per_token ? line_ld(p.d) : p.d;
+  b.tl = teacher_layout(o, p, b.hc_ld);
   if (own_teacher) o = b.tl.end;
   b.off_G = o; o = align256(o + (size_t)b.Tb_pad * b.Vb_pad * 2);
-  b.dH_parts = split_dH ? dH_split(b.Tb, p.d, b.Vb) : 1;
+  b.dH_parts = per_token ? dH_split(b.Tb, p.d, b.Vb) : 1;
   b.off_dH = o; o = align256(o + (size_t)b.dH_parts * p.T * p.d * 4);
   b.total = o;
   return b;
@@ -608,9 +618,9 @@ size_t kd_kl_workspace_size(const kd_kl_problem* prob, int which) {
     // The split count depends on the SM count and the tiling mode; size for
     // the larger of the two modes so the answer holds for either.
     // Pair plans are sized for any number of co-resident clusters up to sms/2.
-    size_t total = plan_forward(*prob, sms, false, sms, mix).total;
+    size_t total = plan_forward(*prob, sms, false, sms, mix, 0, prob->d).total;
     for (int procs = 1; procs <= sms / 2; ++procs)
-      total = std::max(total, plan_forward(*prob, sms, true, procs, mix).total);
+      total = std::max(total, plan_forward(*prob, sms, true, procs, mix, 0, prob->d).total);
     return total;
   }
   if (which == 1 || which == 3) return plan_backward(*prob).total;
@@ -670,7 +680,7 @@ static kd_status forward_impl(const kd_kl_problem* prob, const kd_kl_options* op
   if ((st = get_encoder()) != KD_OK) return st;
   const kd_kl_problem& p = *prob;
   const bool pair = use_pair();
-  const FwdPlan f = plan_forward(p, di.num_sms, pair, gemm_procs(di.num_sms, pair), mix);
+  const FwdPlan f = plan_forward(p, di.num_sms, pair, gemm_procs(di.num_sms, pair), mix, 0, p.d);
   if (workspace_bytes < f.total) return KD_ERR_WORKSPACE;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
   forget_forward(workspace);
@@ -823,11 +833,12 @@ static kd_status backward_blocks(const kd_kl_problem& p, const BwdPlan& b, const
   const bool compact = j.Hc != nullptr;
   const uint16_t* Hop = compact ? j.Hc : j.H;
   const int64_t H_rows = compact ? round_up(p.T, 2 * BM) : p.T;
+  const int64_t H_ld = compact ? b.hc_ld : p.d;
   CUtensorMap tmH_K, tmW_K, tmW_MN, tmH_MN;
-  if (!encode_bf16_2d(&tmH_K, Hop, d, H_rows, d, BK, BM) ||
+  if (!encode_bf16_2d(&tmH_K, Hop, d, H_rows, H_ld, BK, BM) ||
       !encode_bf16_2d(&tmW_K, j.W, d, V, d, BK, pair ? LOGIT_BN / 2 : LOGIT_BN) ||
       !encode_bf16_2d(&tmW_MN, j.W, d, V, d, 64, BK) ||
-      !encode_bf16_2d(&tmH_MN, Hop, d, H_rows, d, 64, BK))
+      !encode_bf16_2d(&tmH_MN, Hop, d, H_rows, H_ld, 64, BK))
     return KD_ERR_CUDA;
 
   // N tile of the dH / dW GEMMs (hidden dimension). 192-wide tiles avoid the
@@ -855,8 +866,11 @@ static kd_status backward_blocks(const kd_kl_problem& p, const BwdPlan& b, const
         // Units of 2 vocabulary tiles: nothing runs across tiles but each
         // row's cursor into its teacher ids, and short units keep the tail
         // of these short launches small.
-        // (One tile for the few units of a short token-gradient launch.)
-        const bool few = j.row_grad && ceil_div(rows, tile_m) * ceil_div(cols, LOGIT_BN) <= 2 * procs;
+        // (One tile for the few units of a short token-gradient launch: 639 tokens
+        // of d = 1000, V = 32,003: 47 us, with two 54; 2048 of d = 2880, V =
+        // 64,000: 444 and 453; from some 32 tiles a processor on level.)
+        const bool few =
+            j.row_grad && ceil_div(rows, tile_m) * ceil_div(cols, LOGIT_BN) <= 32 * (int64_t)procs;
         const LogitPlan lp = plan_logit(rows, cols, d, tile_m, few ? 1 : 2);
         GemmShape sh{};
         sh.inject_stall = stall;
@@ -1052,7 +1066,7 @@ static kd_status backward_impl(const kd_kl_problem* prob, const kd_kl_options* o
   // counted tokens): the forward workspace's, at the same offsets, or
   // prepared here.
   char* tws = reuse ? static_cast<char*>(const_cast<void*>(fwd_ws)) : static_cast<char*>(workspace);
-  const TeacherLayout tl = reuse ? teacher_layout(kHeaderBytes, p) : b.tl;
+  const TeacherLayout tl = reuse ? teacher_layout(kHeaderBytes, p, p.d) : b.tl;
   int32_t* sidx = at<int32_t>(tws, tl.off_sidx);
   float* sp = at<float>(tws, tl.off_sp);
   const bool compact = mask != nullptr;
@@ -1300,8 +1314,9 @@ static kd_status logprob_validate(const kd_logprob_problem* p, const void* H, co
 // costing the epilogue e, a unit's row state s on top and on average half a
 // unit's wait at the end, the time is about n e + n s / u + u e / 2: least at
 // u = sqrt(2 n s / e). s is about 1.3 us (two dependent loads from L2), e 5.4.
-// 8 at most, as in the KL forward. Measured at d = 1000, V = 32,003: the forward
-// of 4096 tokens 215 us with u = 1 (n = 26).
+// 8 at most, as in the KL forward. Measured at d = 1000, V = 32,003, the forward's
+// product: 4096 tokens (n = 26) 176 us with the rule's 4, 173 with 1, 208 with 8;
+// 639 tokens (n = 5) 48 with 2, 47 with 1, 58 with 8.
 static int logprob_split_tiles(const kd_kl_problem& p, bool pair, int procs) {
   const double n = (double)ceil_div(p.V, LOGIT_BN) *
                    (double)std::max<int64_t>(1, ceil_div(p.T, pair ? 2 * BM : BM)) / procs;
@@ -1309,7 +1324,8 @@ static int logprob_split_tiles(const kd_kl_problem& p, bool pair, int procs) {
 }
 
 static FwdPlan plan_logprob(const kd_kl_problem& p, int num_sms, bool pair, int procs) {
-  return plan_forward(p, num_sms, pair, procs, false, logprob_split_tiles(p, pair, procs));
+  return plan_forward(p, num_sms, pair, procs, false, logprob_split_tiles(p, pair, procs),
+                      line_ld(p.d));
 }
 
 size_t kd_logprob_workspace_size(const kd_logprob_problem* prob, int which) {
@@ -1357,10 +1373,12 @@ kd_status kd_logprob_forward(const kd_logprob_problem* prob, const uint16_t* H, 
   const int64_t T_pad = round_up(T, 2 * BM);
   float* zdot = at<float>(workspace, f.off_ent);
   if (compact) KD_CUDA(launch_mask_scan(mask, T, rowmap, invmap, n_count, stream));
-  KD_CUDA(launch_token_rows(H, W, d, ids, rowmap, n_count, T, V, 2 * BM, compact ? Hc : nullptr,
-                            sidx, sp, zdot, status, di.num_sms, stream));
+  const int64_t hc_ld = line_ld(d);
+  const bool copied = compact || hc_ld != d;  // rows in Hc: the counted ones, or off the lines in H
+  KD_CUDA(launch_token_rows(H, W, d, ids, rowmap, n_count, T, V, 2 * BM, copied ? Hc : nullptr,
+                            (int)hc_ld, sidx, sp, zdot, status, di.num_sms, stream));
   CUtensorMap tmH, tmW;
-  if (!encode_bf16_2d(&tmH, compact ? Hc : H, d, compact ? T_pad : T, d, BK, BM) ||
+  if (!encode_bf16_2d(&tmH, copied ? Hc : H, d, copied ? T_pad : T, copied ? hc_ld : d, BK, BM) ||
       !encode_bf16_2d(&tmW, W, d, V, d, BK, pair ? LOGIT_BN / 2 : LOGIT_BN))
     return KD_ERR_CUDA;
   GemmShape sh{};
@@ -1432,8 +1450,8 @@ kd_status kd_logprob_backward(const kd_logprob_problem* prob, const uint16_t* H,
   uint16_t* Hc = at<uint16_t>(workspace, b.tl.off_Hc);
   // Only the tokens with a gradient, as the other calls do with a mask.
   KD_CUDA(launch_grad_scan(grad_logp, T, rowmap, invmap, n_count, stream));
-  KD_CUDA(launch_token_rows(H, W, d, ids, rowmap, n_count, T, V, 2 * BM, Hc, sidx, sp, nullptr,
-                            status, di.num_sms, stream));
+  KD_CUDA(launch_token_rows(H, W, d, ids, rowmap, n_count, T, V, 2 * BM, Hc, (int)b.hc_ld, sidx,
+                            sp, nullptr, status, di.num_sms, stream));
   BackwardBlocks bb{};
   bb.H = H;
   bb.W = W;

@@ -182,11 +182,11 @@ cudaError_t launch_gemm_dw_dh(bool pair, bool dh_first, const CUtensorMap& tmG_M
 cudaError_t launch_grad_scan(const float* grad, int T, int* rowmap, int* invmap, int* n_count,
                              cudaStream_t stream);
 // Row r's id and weight 1 as a teacher row of one entry, its row of H in Hc (or
-// null) and its own logit before scaling in zdot (or null); checks the id.
+// null; hc_ld elements a row) and its own logit before scaling in zdot (or null); checks the id.
 cudaError_t launch_token_rows(const uint16_t* H, const uint16_t* W, int d, const int32_t* ids,
                               const int* rowmap, const int* n_count, int T, int V, int round,
-                              uint16_t* Hc, int32_t* sidx, float* sp, float* zdot, int* status,
-                              int num_sms, cudaStream_t stream);
+                              uint16_t* Hc, int hc_ld, int32_t* sidx, float* sp, float* zdot,
+                              int* status, int num_sms, cudaStream_t stream);
 cudaError_t launch_logp_combine(const float* pm, const float* ps, const float* pd, int nsplit,
                                 int T, const int* invmap, const float* zdot, float cl2,
                                 float inv_tau, float* logp, float* lse, cudaStream_t stream);

@@ -537,8 +537,8 @@ __global__ void __launch_bounds__(SCAN_THREADS)
 __global__ void __launch_bounds__(256)
     token_rows_kernel(const uint4* __restrict__ H, const uint4* __restrict__ W, int row16,
                       const int32_t* __restrict__ ids, const int* rowmap, const int* n_count, int T,
-                      int V, int round, uint4* Hc, int32_t* sidx, float* sp, float* zdot,
-                      int* status) {
+                      int V, int round, uint4* Hc, int hc_ld16, int32_t* sidx, float* sp,
+                      float* zdot, int* status) {
   grid_dependents_go();
   grid_dependency_wait();
   const int lane = threadIdx.x & 31;
@@ -547,7 +547,7 @@ __global__ void __launch_bounds__(256)
   const long long warps = (long long)gridDim.x * (blockDim.x >> 5);
   for (long long r = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); r < end;
        r += warps) {
-    uint4* o = Hc ? Hc + r * row16 : nullptr;
+    uint4* o = Hc ? Hc + r * hc_ld16 : nullptr;
     if (r >= N) {
       for (int c = lane; c < row16; c += 32) o[c] = make_uint4(0u, 0u, 0u, 0u);
       continue;
@@ -977,19 +977,19 @@ cudaError_t launch_grad_scan(const float* grad, int T, int* rowmap, int* invmap,
 
 cudaError_t launch_token_rows(const uint16_t* H, const uint16_t* W, int d, const int32_t* ids,
                               const int* rowmap, const int* n_count, int T, int V, int round,
-                              uint16_t* Hc, int32_t* sidx, float* sp, float* zdot, int* status,
-                              int num_sms, cudaStream_t stream) {
+                              uint16_t* Hc, int hc_ld, int32_t* sidx, float* sp, float* zdot,
+                              int* status, int num_sms, cudaStream_t stream) {
   const int blocks = std::min((T + (Hc ? round : 0) + 7) / 8, num_sms * 8);
   const uint4* h = reinterpret_cast<const uint4*>(H);
   const uint4* w = reinterpret_cast<const uint4*>(W);
   uint4* hc = reinterpret_cast<uint4*>(Hc);
   if (rowmap)  // the scan that wrote it is ahead; without one, nothing of this call's is
     return launch_kernel_early("token_rows", token_rows_kernel, dim3((unsigned)blocks), dim3(256),
-                               0, stream, h, w, d / 8, ids, rowmap, n_count, T, V, round, hc, sidx, sp,
-                               zdot, status);
+                               0, stream, h, w, d / 8, ids, rowmap, n_count, T, V, round, hc, hc_ld / 8,
+                               sidx, sp, zdot, status);
   return launch_kernel("token_rows", token_rows_kernel, dim3((unsigned)blocks), dim3(256), 0,
-                       stream, h, w, d / 8, ids, rowmap, n_count, T, V, round, hc, sidx, sp, zdot,
-                       status);
+                       stream, h, w, d / 8, ids, rowmap, n_count, T, V, round, hc, hc_ld / 8, sidx, sp,
+                       zdot, status);
 }
 
 cudaError_t launch_logp_combine(const float* pm, const float* ps, const float* pd, int nsplit,
