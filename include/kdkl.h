@@ -331,8 +331,11 @@ kd_status kd_logprob_forward(const kd_logprob_problem* prob, const uint16_t* H, 
  *   dH         [T, d] bf16 out
  *   dW         [V, d] out      fp32, overwritten or (accumulate_dW) added to; or bf16
  *                              when prob->dw_bf16 (accumulate_dW must be 0)
- * The gradient of the logits is rounded to bf16 before it enters the two
- * products, as in kd_kl_backward: dH and dW carry that relative 2^-8 per term. */
+ * The entry of each token's own id, g (1 - p) / tau, is taken from its logit and lse
+ * and added in fp32, from first to last: it is off by lse's rounding (g / tau times
+ * 2^-24 |lse|, which is what 1 - p of a confident token is told by) and a few fp32
+ * roundings. The other entries of the logits' gradient, -g p / tau, are rounded to bf16
+ * before they enter the two products: dH and dW carry that relative 2^-8 of those terms. */
 kd_status kd_logprob_backward(const kd_logprob_problem* prob, const uint16_t* H, const uint16_t* W,
                               const int32_t* ids, const float* lse, const float* grad_logp,
                               uint16_t* dH, void* dW, int accumulate_dW, void* workspace,

@@ -259,6 +259,8 @@ struct BwdPlan {
   int64_t hc_ld;
   int dH_parts;  // dH is summed in so many parts of a block's vocabulary
   size_t off_G, off_dH, total;
+  // per token (gradients): each row's own terms (OwnTerms), and the fp32 rows of a bf16 dW
+  size_t off_first, off_idcount, off_coef, off_side;
 };
 
 bool problem_ok(const kd_kl_problem* p) {
@@ -402,12 +404,20 @@ BwdPlan plan_backward(const kd_kl_problem& p, bool own_teacher = true, bool whol
   b.Vb_pad = round_up(b.Vb, LOGIT_BN);
   size_t o = kHeaderBytes;
   b.off_ctr = o; o = align256(o + (size_t)3 * b.n_tblocks * b.n_vblocks * 4);
+  if (per_token) {  // cleared with the header and the counters
+    b.off_first = o; o = align256(o + (size_t)p.V * 4);
+    b.off_idcount = o; o = align256(o + (size_t)p.V * 4);
+  }
   b.hc_ld = per_token ? line_ld(p.d) : p.d;
   b.tl = teacher_layout(o, p, b.hc_ld);
   if (own_teacher) o = b.tl.end;
   b.off_G = o; o = align256(o + (size_t)b.Tb_pad * b.Vb_pad * 2);
   b.dH_parts = per_token ? dH_split(b.Tb, p.d, b.Vb) : 1;
   b.off_dH = o; o = align256(o + (size_t)b.dH_parts * p.T * p.d * 4);
+  if (per_token) {
+    b.off_coef = o; o = align256(o + (size_t)p.T * 4);
+    b.off_side = o; o = align256(o + (whole_dW ? (size_t)p.T * p.d * 4 : 0));
+  }
   b.total = o;
   return b;
 }
@@ -971,10 +981,14 @@ static kd_status backward_blocks(const kd_kl_problem& p, const BwdPlan& b, const
         sh_dw.dyn_dim = 1;  // K: the block's counted tokens
       }
       EpiParams ep_dw{};
-      if (j.dW16)
+      if (j.dW16) {
         ep_dw.out16 = j.dW16 + (int64_t)col0 * d;
-      else
+        ep_dw.T = T;
+        ep_dw.first_row = at<int>(workspace, b.off_first) + col0;
+        ep_dw.side = at<float>(workspace, b.off_side);
+      } else {
         ep_dw.out = j.dW + (int64_t)col0 * d;
+      }
       ep_dw.ldo = d;
       ep_dw.out_rows = cols;
       ep_dw.out_cols = d;
@@ -1376,7 +1390,7 @@ kd_status kd_logprob_forward(const kd_logprob_problem* prob, const uint16_t* H, 
   const int64_t hc_ld = line_ld(d);
   const bool copied = compact || hc_ld != d;  // rows in Hc: the counted ones, or off the lines in H
   KD_CUDA(launch_token_rows(H, W, d, ids, rowmap, n_count, T, V, 2 * BM, copied ? Hc : nullptr,
-                            (int)hc_ld, sidx, sp, zdot, status, di.num_sms, stream));
+                            (int)hc_ld, sidx, sp, zdot, OwnTerms{}, status, di.num_sms, stream));
   CUtensorMap tmH, tmW;
   if (!encode_bf16_2d(&tmH, copied ? Hc : H, d, copied ? T_pad : T, copied ? hc_ld : d, BK, BM) ||
       !encode_bf16_2d(&tmW, W, d, V, d, BK, pair ? LOGIT_BN / 2 : LOGIT_BN))
@@ -1436,7 +1450,7 @@ kd_status kd_logprob_backward(const kd_logprob_problem* prob, const uint16_t* H,
   forget_forward(workspace);
   int* status = at<int>(workspace, 0);
   int* n_count = status + 1;
-  KD_CUDA(cudaMemsetAsync(workspace, 0, b.tl.off_sidx, stream));  // header and unit counters
+  KD_CUDA(cudaMemsetAsync(workspace, 0, b.tl.off_sidx, stream));  // header, unit counters, ids
   if (p.T == 0) {
     if (!accumulate_dW)
       KD_CUDA(cudaMemsetAsync(dW, 0, (size_t)p.V * p.d * (bf16 ? 2 : 4), stream));
@@ -1450,8 +1464,15 @@ kd_status kd_logprob_backward(const kd_logprob_problem* prob, const uint16_t* H,
   uint16_t* Hc = at<uint16_t>(workspace, b.tl.off_Hc);
   // Only the tokens with a gradient, as the other calls do with a mask.
   KD_CUDA(launch_grad_scan(grad_logp, T, rowmap, invmap, n_count, stream));
+  OwnTerms own{};
+  own.lse = lse;
+  own.grad = grad_logp;
+  own.inv_tau = 1.0f / p.temperature;
+  own.coef = at<float>(workspace, b.off_coef);
+  own.first_row = at<int>(workspace, b.off_first);
+  own.id_count = at<int>(workspace, b.off_idcount);
   KD_CUDA(launch_token_rows(H, W, d, ids, rowmap, n_count, T, V, 2 * BM, Hc, (int)b.hc_ld, sidx,
-                            sp, nullptr, status, di.num_sms, stream));
+                            sp, nullptr, own, status, di.num_sms, stream));
   BackwardBlocks bb{};
   bb.H = H;
   bb.W = W;
@@ -1469,8 +1490,10 @@ kd_status kd_logprob_backward(const kd_logprob_problem* prob, const uint16_t* H,
     bb.dW = static_cast<float*>(dW);
   bb.accumulate_dW = accumulate_dW;
   if ((st = backward_blocks(p, b, bb, workspace, di.num_sms, stream)) != KD_OK) return st;
-  KD_CUDA(launch_f32_to_bf16(at<float>(workspace, b.off_dH), dH, (long long)p.T * p.d, d, invmap,
-                             di.num_sms, stream, b.dH_parts, true));
+  KD_CUDA(launch_logprob_finish(at<float>(workspace, b.off_dH), b.dH_parts, dH, W, Hc,
+                                (int)b.hc_ld, invmap, n_count, sidx, T, V, d, own, bb.dW, bb.dW16,
+                                bf16 ? at<float>(workspace, b.off_side) : nullptr, di.num_sms,
+                                stream));
   return KD_OK;
 }
 

@@ -111,10 +111,9 @@ cudaError_t launch_lse_combine_mix(const float* pm, const float* ps, const float
 cudaError_t launch_loss_finalize(const double* block_sums, int nblocks, const int* n_count,
                                  float* loss, cudaStream_t stream);
 // out [T, d] bf16 <- in rows (invmap[t], or t when invmap is nullptr; zeros
-// for invmap[t] < 0); n = T * d; the sum of `parts` such arrays, n apart.
+// for invmap[t] < 0); n = T * d.
 cudaError_t launch_f32_to_bf16(const float* in, uint16_t* out, long long n, int d,
-                               const int* invmap, int num_sms, cudaStream_t stream, int parts = 1,
-                               bool early = false);
+                               const int* invmap, int num_sms, cudaStream_t stream);
 // merge of per-split top-K lists; shared memory = topk_merge_p2() * 8 bytes
 int topk_merge_p2(int nsplit, int K);
 cudaError_t launch_topk_merge(const float* unit_val, const int32_t* unit_id, const int* unit_cnt,
@@ -181,12 +180,29 @@ cudaError_t launch_gemm_dw_dh(bool pair, bool dh_first, const CUtensorMap& tmG_M
 // Compaction of the tokens whose gradient is not zero (NaN included).
 cudaError_t launch_grad_scan(const float* grad, int T, int* rowmap, int* invmap, int* n_count,
                              cudaStream_t stream);
-// Row r's id and weight 1 as a teacher row of one entry, its row of H in Hc (or
-// null; hc_ld elements a row) and its own logit before scaling in zdot (or null); checks the id.
+// What the backward adds to dH and dW for each row's own id, in fp32.
+struct OwnTerms {
+  const float *lse, *grad;  // [T] per caller token (inputs)
+  float inv_tau;
+  float* coef;      // [T] row r: grad / tau * (1 - p of its id)
+  int* first_row;   // [V] T - the first row with this id, 0: none (zero before)
+  int* id_count;    // [V] rows with this id (zero before)
+};
+// Row r's id and weight 1 as a teacher row of one entry, its row of H in Hc (or null;
+// hc_ld elements a row) and its own logit before scaling: in zdot (the forward), or as
+// the coefficient in `own` (the backward). Checks the id.
 cudaError_t launch_token_rows(const uint16_t* H, const uint16_t* W, int d, const int32_t* ids,
                               const int* rowmap, const int* n_count, int T, int V, int round,
                               uint16_t* Hc, int hc_ld, int32_t* sidx, float* sp, float* zdot,
-                              int* status, int num_sms, cudaStream_t stream);
+                              const OwnTerms& own, int* status, int num_sms, cudaStream_t stream);
+// dH [T, d] bf16 from `parts` fp32 arrays [T, d] and the rows' own terms (zeros where
+// invmap < 0); the own terms added to dW's rows: in place (fp32), or with the fp32 rows
+// of `side` rounded into dW16.
+cudaError_t launch_logprob_finish(const float* dH_acc, int parts, uint16_t* dH, const uint16_t* W,
+                                  const uint16_t* Hc, int hc_ld, const int* invmap,
+                                  const int* n_count, const int32_t* sidx, int T, int V, int d,
+                                  const OwnTerms& own, float* dW, uint16_t* dW16, const float* side,
+                                  int num_sms, cudaStream_t stream);
 cudaError_t launch_logp_combine(const float* pm, const float* ps, const float* pd, int nsplit,
                                 int T, const int* invmap, const float* zdot, float cl2,
                                 float inv_tau, float* logp, float* lse, cudaStream_t stream);

@@ -406,45 +406,191 @@ __global__ void __launch_bounds__(1024)
 }
 
 // out row t = bf16(in row invmap[t]), or zeros when invmap[t] < 0; invmap
-// nullptr: row t. One block per row at a time, d4 = d / 4 float4 per row. With
-// more than one part (part_stride4 float4 apart) the row is their sum, in order.
-// (The inputs are not __restrict__: their loads must stay behind the wait.)
-__global__ void f32_to_bf16_kernel(const float4* in, uint2* __restrict__ out, int T, int d4,
-                                   const int* invmap, int parts, long long part_stride4) {
-  grid_dependency_wait();
+// nullptr: row t. One block per row at a time, d4 = d / 4 float4 per row.
+__global__ void f32_to_bf16_kernel(const float4* __restrict__ in, uint2* __restrict__ out, int T,
+                                   int d4, const int* __restrict__ invmap) {
   for (int t = blockIdx.x; t < T; t += gridDim.x) {
-    const int r = invmap ? invmap[t] : t;
+    const int r = invmap ? __ldg(invmap + t) : t;
     uint2* o = out + (long long)t * d4;
     if (r < 0) {
       for (int c = threadIdx.x; c < d4; c += blockDim.x) o[c] = make_uint2(0u, 0u);
       continue;
     }
     const float4* src = in + (long long)r * d4;
-    if (parts == 1) {
-      for (int c0 = threadIdx.x; c0 < d4; c0 += 4 * blockDim.x) {  // four loads in flight
-        float4 v[4];
+    for (int c0 = threadIdx.x; c0 < d4; c0 += 4 * blockDim.x) {  // four loads in flight
+      float4 v[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (c0 + k * (int)blockDim.x < d4) v[k] = __ldcs(src + c0 + k * blockDim.x);
+      for (int k = 0; k < 4; ++k)
+        if (c0 + k * (int)blockDim.x < d4) v[k] = __ldcs(src + c0 + k * blockDim.x);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (c0 + k * (int)blockDim.x < d4)
-            o[c0 + k * blockDim.x] =
-                make_uint2(pack_bf16x2(v[k].x, v[k].y), pack_bf16x2(v[k].z, v[k].w));
+      for (int k = 0; k < 4; ++k)
+        if (c0 + k * (int)blockDim.x < d4)
+          o[c0 + k * blockDim.x] =
+              make_uint2(pack_bf16x2(v[k].x, v[k].y), pack_bf16x2(v[k].z, v[k].w));
+    }
+  }
+}
+
+// v += a * four bf16 values.
+__device__ __forceinline__ void add_bf16x4(float4& v, float a, uint2 w) {
+  v.x = fmaf(a, __uint_as_float(w.x << 16), v.x);
+  v.y = fmaf(a, __uint_as_float(w.x & 0xffff0000u), v.y);
+  v.z = fmaf(a, __uint_as_float(w.y << 16), v.z);
+  v.w = fmaf(a, __uint_as_float(w.y & 0xffff0000u), v.w);
+}
+
+// The end of the log-probabilities' backward. The gradient of the logits entered the
+// products with a zero at each row's own id: that entry, coef = g (1 - p) / tau, is
+// most of the gradient, and cancels for a confident token, so it stays in fp32 and its
+// terms are added here:
+//   dW[v] += sum over the rows r of id v of coef[r] H[r]   items 0 .. N - 1
+//   dH[t] = bf16(sum of the parts + coef[r] W[id])         items N .. N + T - 1
+// An item is a block's. That of row r works on dW if r is its id's first row (others
+// end at once), and finds the id's other rows, in order, in the ids after r: 2048 or
+// 4096 at a time, as many as it knows to be there, so an id that occurs once costs no
+// search. A frequent id is a chain of loads, which the other items hide if it is short:
+// eight of its rows of H are on their way at a time, for narrow rows in several strands
+// that are added up in order at the end. The order of every sum is fixed. A bf16 dW
+// takes the product's rows in fp32 from `side`. What bounds it is the chain of lookups
+// (row, id, first row, coefficient) of each item: 56 us for 3000 of 6000 tokens of
+// d = 2880, beside 8.5 ms of products. 256 threads a block, or 128 for d up to 512, where
+// more would idle (2655 tokens of d = 184, V = 17,389 with the forward: 163 and 159 us;
+// 639 of d = 1000, V = 32,003: 195 and 197).
+template <int FINISH_THREADS>
+__global__ void __launch_bounds__(FINISH_THREADS, 1024 / FINISH_THREADS)
+    logprob_finish_kernel(const float4* dH_acc, int parts, long long part_stride4, uint2* dH,
+                          const uint2* W, const uint2* Hc, int hc_ld4, const int* invmap,
+                          const int* n_count, const int32_t* sidx, int T, int V, int d4,
+                          const OwnTerms own, float4* dW, uint2* dW16, const float4* side) {
+  constexpr int WARPS = FINISH_THREADS / 32, STEPS = 16, SPAN = STEPS * FINISH_THREADS;
+  constexpr int FLIGHT = 8;
+  constexpr int PIECES = STEPS * WARPS / 32;  // of 32 ids, a lane
+  __shared__ uint32_t found[STEPS * WARPS];
+  __shared__ int row_of[SPAN];
+  __shared__ float4 strand_sum[FINISH_THREADS];
+  grid_dependency_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int N = min(*n_count, T);
+  const int strands = d4 < FINISH_THREADS ? FINISH_THREADS / d4 : 1;
+  const int strand = d4 < FINISH_THREADS ? tid / d4 : 0;
+  for (long long item = blockIdx.x; item < (long long)T + N; item += gridDim.x) {
+    if (item >= N) {
+      const int t = (int)(item - N), r = invmap[t];
+      uint2* o = dH + (long long)t * d4;
+      if (r < 0) {
+        for (int c = tid; c < d4; c += FINISH_THREADS) o[c] = make_uint2(0u, 0u);
+        continue;
+      }
+      const float4* src = dH_acc + (long long)r * d4;
+      const int id = sidx[r];
+      const bool known = id >= 0 && id < V;
+      const uint2* w = W + (long long)(known ? id : 0) * d4;
+      const float a = known ? own.coef[r] : 0.f;
+      for (int c = tid; c < d4; c += FINISH_THREADS) {
+        float4 v = src[c];
+        const uint2 x = __ldg(w + c);
+#pragma unroll 4
+        for (int k = 1; k < parts; ++k) {
+          const float4 p = src[k * part_stride4 + c];
+          v.x += p.x;
+          v.y += p.y;
+          v.z += p.z;
+          v.w += p.w;
+        }
+        if (known) add_bf16x4(v, a, x);
+        o[c] = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
       }
       continue;
     }
-    for (int c = threadIdx.x; c < d4; c += blockDim.x) {
-      float4 v = src[c];
-#pragma unroll 4
-      for (int k = 1; k < parts; ++k) {
-        const float4 p = src[k * part_stride4 + c];
-        v.x += p.x;
-        v.y += p.y;
-        v.z += p.z;
-        v.w += p.w;
+    const int r = (int)item;
+    const int id = sidx[r];
+    if (id < 0 || id >= V || own.first_row[id] != T - r) continue;  // the whole block
+    const int others = own.id_count[id] - 1;
+    const float a = own.coef[r];
+    // 4 columns a thread
+    for (int c0 = 0; c0 < d4; c0 += FINISH_THREADS) {
+      const int c = c0 + tid - strand * d4;
+      const bool mine = strand < strands && c < d4;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (mine && strand == 0) {
+        v = side ? side[(long long)r * d4 + c] : dW[(long long)id * d4 + c];
+        add_bf16x4(v, a, Hc[(long long)r * hc_ld4 + c]);
       }
-      o[c] = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+      int left = others;
+      for (long long base = r + 1ll; left > 0 && base < N; base += SPAN) {
+        uint32_t is = 0;  // bit k: step k's id is the one
+#pragma unroll
+        for (int k = 0; k < STEPS; ++k) {
+          const long long i = base + k * FINISH_THREADS + tid;
+          is |= (i < N && sidx[i] == id ? 1u : 0u) << k;
+        }
+#pragma unroll
+        for (int k = 0; k < STEPS; ++k) {
+          const uint32_t m = __ballot_sync(0xffffffffu, (is >> k) & 1u);
+          if (lane == 0) found[k * WARPS + warp] = m;
+        }
+        __syncthreads();
+        // The rows found, in order: piece q = k * WARPS + warp holds 32 ids. A lane adds
+        // up PIECES of them; those of its own that are before its warp's, apart.
+        int sum = 0, ahead = 0;
+#pragma unroll
+        for (int j = 0; j < PIECES; ++j) {
+          const int n = __popc(found[PIECES * lane + j]);
+          sum += n;
+          if (j < warp % PIECES) ahead += n;
+        }
+        int before = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int up = __shfl_up_sync(0xffffffffu, before, o);
+          if (lane >= o) before += up;
+        }
+        const int n = __shfl_sync(0xffffffffu, before, 31);
+        before += ahead - sum;
+        for (int k = 0; k < STEPS; ++k) {
+          const int q = k * WARPS + warp;
+          const int at = __shfl_sync(0xffffffffu, before, q / PIECES);
+          if ((is >> k) & 1u)
+            row_of[at + __popc(found[q] & ((1u << lane) - 1u))] =
+                (int)(base + k * FINISH_THREADS + tid);
+        }
+        __syncthreads();
+        left -= n;
+        for (int j = strand; mine && j < n; j += FLIGHT * strands) {
+          uint2 x[FLIGHT];
+          float f[FLIGHT];
+#pragma unroll
+          for (int k = 0; k < FLIGHT; ++k)
+            if (j + k * strands < n) {
+              const int i = row_of[j + k * strands];
+              x[k] = Hc[(long long)i * hc_ld4 + c];
+              f[k] = own.coef[i];
+            }
+#pragma unroll
+          for (int k = 0; k < FLIGHT; ++k)
+            if (j + k * strands < n) add_bf16x4(v, f[k], x[k]);
+        }
+        __syncthreads();  // before the list is written again
+      }
+      if (others > 0 && strands > 1) {
+        strand_sum[tid] = v;
+        __syncthreads();
+        if (mine && strand == 0)
+          for (int k = 1; k < strands; ++k) {
+            const float4 p = strand_sum[k * d4 + c];
+            v.x += p.x;
+            v.y += p.y;
+            v.z += p.z;
+            v.w += p.w;
+          }
+        __syncthreads();  // before it is written again
+      }
+      if (mine && strand == 0) {
+        if (side)
+          dW16[(long long)id * d4 + c] = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+        else
+          dW[(long long)id * d4 + c] = v;
+      }
     }
   }
 }
@@ -532,13 +678,15 @@ __global__ void __launch_bounds__(SCAN_THREADS)
 // A row per counted token, a warp each: the token's id with weight 1 as a
 // teacher row of one entry, so that the GEMM epilogues pick z at that id and
 // subtract its one-hot; with Hc, the token's row of H copied there (rows from N
-// to the end of N's last tile of `round` are zeroed); with zdot, the id's logit
-// before scaling, H row . W row in fp32 (a lane's products, then a tree).
+// to the end of N's last tile of `round` are zeroed); the id's logit before scaling,
+// H row . W row in fp32 (a lane's products, then a tree): into zdot, or (zdot null)
+// with the token's lse and gradient the coefficient of the row's own terms,
+// g (1 - p) / tau = -g expm1(z / tau - lse) / tau, and its id's first row and count.
 __global__ void __launch_bounds__(256)
     token_rows_kernel(const uint4* __restrict__ H, const uint4* __restrict__ W, int row16,
                       const int32_t* __restrict__ ids, const int* rowmap, const int* n_count, int T,
                       int V, int round, uint4* Hc, int hc_ld16, int32_t* sidx, float* sp,
-                      float* zdot, int* status) {
+                      float* zdot, const OwnTerms own, int* status) {
   grid_dependents_go();
   grid_dependency_wait();
   const int lane = threadIdx.x & 31;
@@ -567,23 +715,24 @@ __global__ void __launch_bounds__(256)
     for (int c = lane; c < row16; c += 32) {
       const uint4 x = __ldg(h + c);
       if (o) o[c] = x;
-      if (zdot) {
-        const uint4 y = __ldg(w + c);
-        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-        float part = 0.f;
+      const uint4 y = __ldg(w + c);
+      const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+      float part = 0.f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          part = fmaf(__uint_as_float(xs[k] << 16), __uint_as_float(ys[k] << 16), part);
-          part = fmaf(__uint_as_float(xs[k] & 0xffff0000u), __uint_as_float(ys[k] & 0xffff0000u),
-                      part);
-        }
-        dot += part;
+      for (int k = 0; k < 4; ++k) {
+        part = fmaf(__uint_as_float(xs[k] << 16), __uint_as_float(ys[k] << 16), part);
+        part = fmaf(__uint_as_float(xs[k] & 0xffff0000u), __uint_as_float(ys[k] & 0xffff0000u),
+                    part);
       }
+      dot += part;
     }
-    if (zdot) {
 #pragma unroll
-      for (int k = 16; k > 0; k >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, k);
-      if (lane == 0) zdot[r] = dot;
+    for (int k = 16; k > 0; k >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, k);
+    if (lane == 0 && zdot) zdot[r] = dot;
+    if (lane == 0 && !zdot && known) {
+      own.coef[r] = -own.grad[tok] * own.inv_tau * expm1f(fmaf(dot, own.inv_tau, -own.lse[tok]));
+      atomicMax(own.first_row + id, T - (int)r);
+      atomicAdd(own.id_count + id, 1);
     }
   }
 }
@@ -956,17 +1105,29 @@ cudaError_t launch_gather_rows(const uint16_t* H, int d, const int* rowmap, cons
 }
 
 cudaError_t launch_f32_to_bf16(const float* in, uint16_t* out, long long n, int d,
-                               const int* invmap, int num_sms, cudaStream_t stream, int parts,
-                               bool early) {
+                               const int* invmap, int num_sms, cudaStream_t stream) {
   const int T = (int)(n / d);  // n = T * d, d a multiple of 8
   const int blocks = std::max(1, std::min(T, num_sms * 8));
-  if (early)
-    return launch_kernel_early("f32_to_bf16", f32_to_bf16_kernel, dim3((unsigned)blocks), dim3(256),
-                               0, stream, reinterpret_cast<const float4*>(in),
-                               reinterpret_cast<uint2*>(out), T, d / 4, invmap, parts, n / 4);
   return launch_kernel("f32_to_bf16", f32_to_bf16_kernel, dim3((unsigned)blocks), dim3(256), 0,
                        stream, reinterpret_cast<const float4*>(in), reinterpret_cast<uint2*>(out),
-                       T, d / 4, invmap, parts, n / 4);
+                       T, d / 4, invmap);
+}
+
+cudaError_t launch_logprob_finish(const float* dH_acc, int parts, uint16_t* dH, const uint16_t* W,
+                                  const uint16_t* Hc, int hc_ld, const int* invmap,
+                                  const int* n_count, const int32_t* sidx, int T, int V, int d,
+                                  const OwnTerms& own, float* dW, uint16_t* dW16, const float* side,
+                                  int num_sms, cudaStream_t stream) {
+  const bool narrow = d <= 512;
+  const auto kernel = narrow ? logprob_finish_kernel<128> : logprob_finish_kernel<256>;
+  const int blocks = (int)std::min<long long>(2ll * T, (long long)num_sms * (narrow ? 16 : 8));
+  return launch_kernel_early(
+      "logprob_finish", kernel, dim3((unsigned)blocks), dim3(narrow ? 128 : 256), 0, stream,
+      reinterpret_cast<const float4*>(dH_acc), parts, (long long)T * d / 4,
+      reinterpret_cast<uint2*>(dH), reinterpret_cast<const uint2*>(W),
+      reinterpret_cast<const uint2*>(Hc), hc_ld / 4, invmap, n_count, sidx, T, V, d / 4, own,
+      reinterpret_cast<float4*>(dW), reinterpret_cast<uint2*>(dW16),
+      reinterpret_cast<const float4*>(side));
 }
 
 cudaError_t launch_grad_scan(const float* grad, int T, int* rowmap, int* invmap, int* n_count,
@@ -978,7 +1139,7 @@ cudaError_t launch_grad_scan(const float* grad, int T, int* rowmap, int* invmap,
 cudaError_t launch_token_rows(const uint16_t* H, const uint16_t* W, int d, const int32_t* ids,
                               const int* rowmap, const int* n_count, int T, int V, int round,
                               uint16_t* Hc, int hc_ld, int32_t* sidx, float* sp, float* zdot,
-                              int* status, int num_sms, cudaStream_t stream) {
+                              const OwnTerms& own, int* status, int num_sms, cudaStream_t stream) {
   const int blocks = std::min((T + (Hc ? round : 0) + 7) / 8, num_sms * 8);
   const uint4* h = reinterpret_cast<const uint4*>(H);
   const uint4* w = reinterpret_cast<const uint4*>(W);
@@ -986,10 +1147,10 @@ cudaError_t launch_token_rows(const uint16_t* H, const uint16_t* W, int d, const
   if (rowmap)  // the scan that wrote it is ahead; without one, nothing of this call's is
     return launch_kernel_early("token_rows", token_rows_kernel, dim3((unsigned)blocks), dim3(256),
                                0, stream, h, w, d / 8, ids, rowmap, n_count, T, V, round, hc, hc_ld / 8,
-                               sidx, sp, zdot, status);
+                               sidx, sp, zdot, own, status);
   return launch_kernel("token_rows", token_rows_kernel, dim3((unsigned)blocks), dim3(256), 0,
                        stream, h, w, d / 8, ids, rowmap, n_count, T, V, round, hc, hc_ld / 8, sidx, sp,
-                       zdot, status);
+                       zdot, own, status);
 }
 
 cudaError_t launch_logp_combine(const float* pm, const float* ps, const float* pd, int nsplit,

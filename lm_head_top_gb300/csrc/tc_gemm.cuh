@@ -180,12 +180,19 @@ struct EpiParams {
   const uint8_t* mask;  // may be null (all tokens count)
   const int* n_count;   // number of counted tokens N
   float g_over_tau;
-  const float* row_grad;  // per caller token, or null: the row's scale is -row_grad * g_over_tau
+  // Per caller token, or null: the row's scale is -row_grad * g_over_tau, and the
+  // entry of the row's one id is left at zero (its term is added in fp32 later, see
+  // logprob_finish).
+  const float* row_grad;
   uint16_t* G;   // bf16 bits, [rows_pad, ldg]
   int64_t ldg;
   // EPI_STORE
   float* out;
   uint16_t* out16;  // bf16 output instead of `out` (stored, not accumulated), or null
+  // With out16: output rows with first_row[r] != 0 also go to row T - first_row[r] of
+  // `side` in fp32, for what is added to them before they are rounded. Or null.
+  const int* first_row;
+  float* side;
   int64_t ldo;
   int64_t part_stride;  // elements between the outputs of K parts
   int out_rows, out_cols;
@@ -864,6 +871,11 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
           th = topk_shared_threshold(rkey);
         }
       }
+      float* side_row = nullptr;  // EPI_STORE: see EpiParams::side
+      if (EPI == EPI_STORE && eo.first_row && r < eo.out_rows) {
+        const int left = eo.first_row[r];
+        if (left) side_row = eo.side + (long long)(eo.T - left) * eo.ldo;
+      }
       // MIX row state: temperature-1 sum, label logit, label id
       float run_s1 = 0.f, zl = 0.f, lse12 = 0.f, w_kl = 0.f, w_ce = 0.f;
       int lab = -1;
@@ -1024,7 +1036,11 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
               // zeros: their teacher rows are never read (cursor stays at K)
               const int vend = ep.col0 + min(cl + 32, ep.cols);
               while (cur_id < vend) {
-                if (cur_id >= vid0) {
+                if (!MIX && ep.row_grad) {  // one id a row
+                  const int jj = cur_id - vid0;
+#pragma unroll
+                  for (int j = 0; j < 32; ++j) g[j] = (j == jj) ? 0.f : g[j];
+                } else if (cur_id >= vid0) {
                   const float pk = MIX ? __ldg(p_row + cursor) * w_kl : __ldg(p_row + cursor);
                   const int jj = cur_id - vid0;
 #pragma unroll
@@ -1058,6 +1074,13 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
           } else {  // EPI_STORE
             const int r0 = r - lane;
             if (eo.out16) {
+              if (side_row) {  // few rows have own terms
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  if (cl + 4 * j < eo.out_cols)
+                    *reinterpret_cast<float4*>(side_row + cl + 4 * j) =
+                        make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+              }
               stage_bf16(v, 4 * (c & 1));
               if ((c & 1) || cl + 32 >= eo.out_cols) {
                 const int cb = cl - 32 * (c & 1);
