@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(SEQ_THREADS, SEQ_RESIDENT)
           const float d = counts ? lp[j] - lo[j] : 0.f;
           const float side = pos ? d : -d, border = pos ? a.high_hi : -a.low_hi;
           clip = side > border;
-          if (side == border)  // hardly ever
+          if (counts && side == border)  // hardly ever (what is not counted may not be looked at)
             clip = pos ? exceeds(d, lp[j], lo[j], a.high_hi, a.high_lo)
                        : exceeds(-d, lo[j], lp[j], -a.low_hi, -a.low_lo);
           r = clip ? (pos ? a.r_high : a.r_low) : exp_fast(d);
