@@ -61,7 +61,8 @@ def main():
             note = "chosen above rejected %.2f" % (rewards[:, 0] > rewards[:, 1]).float().mean().item()
         else:
             loss, stats, grad = kdkl.kd_policy_loss(logp, old_logp, ref_logp, advantages, mask, cu_seqlens,
-                                                    clip_high=0.28, kl_coef=0.02, reduction="sequence")
+                                                    advantage_per_sequence=True, clip_high=0.28, kl_coef=0.02,
+                                                    reduction="sequence")
             note = "KL %.4f, clipped %.2f" % (stats[1].item(), stats[2].item())
         kdkl.kd_logprob_backward(H, W, ids, lse, grad, dW=dW)
         kdkl.kd_adamw_step(tensors, lr=a.lr, betas=(0.9, 0.95), step=step)

@@ -618,13 +618,15 @@ def kd_logprob_backward(H, W, ids, lse, grad_logp, *, temperature=1.0, chunk=409
 
 
 def kd_policy_loss(logp, old_logp, ref_logp, advantages, mask=None, cu_seqlens=None, *,
-                   clip_low=0.2, clip_high=0.2, dual_clip=0.0, kl_coef=0.0, reduction="token",
-                   norm=1.0, grad_loss=1.0, want_grad=True, loss=None, stats=None, grad_logp=None,
-                   workspace=None, stream=None):
+                   advantage_per_sequence=None, clip_low=0.2, clip_high=0.2, dual_clip=0.0,
+                   kl_coef=0.0, reduction="token", norm=1.0, grad_loss=1.0, want_grad=True,
+                   loss=None, stats=None, grad_logp=None, workspace=None, stream=None):
     """Clipped policy loss with a KL term over packed sequences, and its gradient.
 
     logp, old_logp (None: ratio 1), ref_logp (None: no KL term): [T] fp32.
-    advantages: [T], or one per sequence of ``cu_seqlens`` ([S+1] int32).
+    advantages: [T], or one per sequence of ``cu_seqlens`` ([S+1] int32): told by
+    their number, or by ``advantage_per_sequence``, which has to be given where there
+    are as many sequences as tokens.
     reduction: "token" (mean over counted tokens), "sequence" (mean over the
     sequences of each one's mean) or "sum" (sum / ``norm``).
     Returns (loss [1], stats [3] = policy part, KL part, share of clipped tokens,
@@ -633,7 +635,18 @@ def kd_policy_loss(logp, old_logp, ref_logp, advantages, mask=None, cu_seqlens=N
     dev = logp.device
     f32, flat = torch.float32, (T,)
     S = 0 if cu_seqlens is None else max(0, cu_seqlens.numel() - 1)
-    per_sequence = cu_seqlens is not None and advantages.numel() == S and S != T
+    per_sequence = advantage_per_sequence
+    if per_sequence is None:
+        if S == T and S > 1 and cu_seqlens is not None:
+            raise ValueError("%d sequences and as many tokens: advantage_per_sequence says which "
+                             "of the two the advantages are for" % S)
+        per_sequence = cu_seqlens is not None and advantages.numel() == S and S != T
+    elif per_sequence and cu_seqlens is None:
+        raise ValueError("advantages per sequence need cu_seqlens")
+    if advantages.numel() != (S if per_sequence else T):
+        raise ValueError("advantages has %d values, expected %d, one per %s"
+                         % ((advantages.numel(),) + ((S, "sequence") if per_sequence
+                                                     else (T, "token"))))
     given = (_addr(logp, "logp", f32, flat, dev), _addr(old_logp, "old_logp", f32, flat, dev),
              _addr(ref_logp, "ref_logp", f32, flat, dev),
              _addr(advantages, "advantages", f32, (S if per_sequence else T,), dev),

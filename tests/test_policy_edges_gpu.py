@@ -60,3 +60,23 @@ def test_clip_range_of_zero_counts_counted_tokens(kdkl, clip_low, clip_high, red
                               clip_high=clip_high, dual_clip=0.0, kl_coef=0.0, reduction=reduction,
                               norm=1.0)
         assert abs(stats[2].item() - want[1][2]) <= 2.0 ** -24
+
+
+@pytest.mark.parametrize("reduction", ["token", "sequence"])
+@pytest.mark.parametrize("T", [2, 9, 700, 6001])
+def test_as_many_sequences_as_tokens(kdkl, reduction, T):
+    """Some sequences empty, others longer: either meaning of T advantages, told by the
+    word. A token's gradient is the same product whichever array its advantage is from."""
+    r = np.random.default_rng(T)
+    logp = (-3 * r.random(T)).astype(np.float32)
+    old = (logp + 0.3 * r.normal(size=T)).astype(np.float32)
+    cu, adv = _ragged(T, T, r), r.normal(size=T).astype(np.float32)
+    seq = np.searchsorted(cu[1:], np.arange(T), side="right")
+    args = [_cuda(logp), _cuda(old), None]
+    kw = dict(reduction=reduction)
+    a = kdkl.kd_policy_loss(*args, _cuda(adv), None, _cuda(cu), advantage_per_sequence=True, **kw)
+    b = kdkl.kd_policy_loss(*args, _cuda(adv[seq]), None, _cuda(cu), advantage_per_sequence=False,
+                            **kw)
+    c = kdkl.kd_policy_loss(*args, _cuda(adv), None, _cuda(cu), advantage_per_sequence=False, **kw)
+    assert torch.equal(a[2], b[2]) and torch.equal(a[1], b[1]) and torch.equal(a[0], b[0])
+    assert torch.equal(a[2], c[2]) == (seq == np.arange(T)).all()  # one token each: the same
