@@ -623,7 +623,7 @@ def kd_policy_loss(logp, old_logp, ref_logp, advantages, mask=None, cu_seqlens=N
                    loss=None, stats=None, grad_logp=None, workspace=None, stream=None):
     """Clipped policy loss with a KL term over packed sequences, and its gradient.
 
-    logp, old_logp (None: ratio 1), ref_logp (None: no KL term): [T] fp32.
+    logp, old_logp (None: ratio 1), ref_logp (None: no KL term, ``kl_coef`` 0): [T] fp32.
     advantages: [T], or one per sequence of ``cu_seqlens`` ([S+1] int32): told by
     their number, or by ``advantage_per_sequence``, which has to be given where there
     are as many sequences as tokens.
@@ -635,6 +635,8 @@ def kd_policy_loss(logp, old_logp, ref_logp, advantages, mask=None, cu_seqlens=N
     dev = logp.device
     f32, flat = torch.float32, (T,)
     S = 0 if cu_seqlens is None else max(0, cu_seqlens.numel() - 1)
+    if ref_logp is None and kl_coef != 0:
+        raise ValueError("a KL term (kl_coef %r) needs ref_logp" % kl_coef)
     per_sequence = advantage_per_sequence
     if per_sequence is None:
         if S == T and S > 1 and cu_seqlens is not None:
@@ -654,8 +656,8 @@ def kd_policy_loss(logp, old_logp, ref_logp, advantages, mask=None, cu_seqlens=N
              _addr(cu_seqlens, "cu_seqlens", torch.int32, (S + 1,), dev))
     if reduction not in KD_REDUCTIONS:
         raise ValueError("reduction must be one of %s, got %r" % (sorted(KD_REDUCTIONS), reduction))
-    p = kd_policy_problem(T, S, clip_low, clip_high, dual_clip, kl_coef if ref_logp is not None
-                          else 0.0, norm, KD_REDUCTIONS[reduction], 1 if per_sequence else 0)
+    p = kd_policy_problem(T, S, clip_low, clip_high, dual_clip, kl_coef, norm,
+                          KD_REDUCTIONS[reduction], 1 if per_sequence else 0)
     need = load().kd_policy_workspace_size(ctypes.byref(p))
     workspace = _given_workspace(workspace, need or 256, "", dev, stream)  # 0: the call says why
     loss = _outcome(loss, "loss", f32, (1,), dev, stream)

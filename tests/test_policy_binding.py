@@ -45,3 +45,10 @@ def test_sizes_that_differ_need_no_word():
 def test_one_sequence_of_one_token_needs_no_word():
     one = torch.zeros(1)
     _refused("CUDA", one, None, None, one, None, torch.tensor([0, 1], dtype=torch.int32))
+
+
+@pytest.mark.parametrize("kl_coef", [0.1, -0.1])
+def test_a_kl_term_needs_its_reference(kl_coef):
+    _refused("ref_logp", X, X, None, X, kl_coef=kl_coef)
+    _refused("CUDA", X, X, None, X, kl_coef=0.0)
+    _refused("CUDA", X, X, X, X, kl_coef=kl_coef)
