@@ -164,8 +164,9 @@ kd_status kd_kl_backward_ex(const kd_kl_problem* prob, const kd_kl_options* opts
  *                  stream and not reused since; read only
  *   workspace      kd_kl_workspace_size(prob, 4) bytes (no teacher region)
  * The library remembers, on the host, which problem each forward workspace
- * was last filled for; a fwd_workspace it does not know for this problem, or
- * fwd_workspace_bytes smaller than that call's, returns KD_ERR_INVALID_ARG
+ * was last filled for, until any call is given that workspace as its own; a
+ * fwd_workspace it does not know for this problem, or that is also `workspace`,
+ * or fwd_workspace_bytes smaller than that call's, returns KD_ERR_INVALID_ARG
  * synchronously. The teacher cache was validated by the forward: its
  * device-detected errors are read from fwd_workspace, this call's (wait
  * timeouts) from workspace. */

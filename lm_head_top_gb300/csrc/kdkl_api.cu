@@ -542,8 +542,9 @@ T* at(void* ws, size_t off) {
 
 // Forward workspaces whose prepared teacher cache a backward may reuse: the
 // problem each one was last filled for by a forward call that queued all its
-// work. A forward call drops its workspace's entry when it starts and adds it
-// back when it has queued everything, so a failed call leaves none.
+// work. Every call drops its workspace's entry before it queues anything, since
+// it overwrites what the forward left there; a forward adds it back when it has
+// queued everything, so a failed call leaves none.
 struct FwdRecord {
   const void* ws;
   int64_t T, d, V;
@@ -556,6 +557,8 @@ constexpr size_t kMaxFwdRecords = 64;
 std::mutex g_fwd_mu;
 std::vector<FwdRecord> g_fwd_records;
 
+}  // namespace
+
 void forget_forward(const void* ws) {
   std::lock_guard<std::mutex> lk(g_fwd_mu);
   for (size_t i = 0; i < g_fwd_records.size(); ++i)
@@ -564,6 +567,8 @@ void forget_forward(const void* ws) {
       return;
     }
 }
+
+namespace {
 
 void remember_forward(const void* ws, const kd_kl_problem& p, size_t bytes, const void* mask) {
   std::lock_guard<std::mutex> lk(g_fwd_mu);
@@ -1048,7 +1053,8 @@ static kd_status backward_impl(const kd_kl_problem* prob, const kd_kl_options* o
   kd_status st = validate_common(prob, H, W, reuse ? fwd_ws : topk_idx,
                                  reuse ? fwd_ws : topk_logit, workspace);
   if (st != KD_OK) return st;
-  if (reuse && !forward_matches(fwd_ws, fwd_ws_bytes, *prob, mask)) return KD_ERR_INVALID_ARG;
+  if (reuse && (fwd_ws == workspace || !forward_matches(fwd_ws, fwd_ws_bytes, *prob, mask)))
+    return KD_ERR_INVALID_ARG;
   const bool mix = opts != nullptr;
   if (mix && ((st = validate_options(prob, opts)) != KD_OK)) return st;
   // temperature-1 logsumexp: needed when the CE term is on and tau != 1
@@ -1065,6 +1071,7 @@ static kd_status backward_impl(const kd_kl_problem* prob, const kd_kl_options* o
   const BwdPlan b = plan_backward(p, !reuse);
   if (workspace_bytes < b.total) return KD_ERR_WORKSPACE;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  forget_forward(workspace);
 
   int* status = at<int>(workspace, 0);
   // the counted-token total N: this call's own, or the forward's
@@ -1184,6 +1191,7 @@ kd_status kd_rkl_forward(const kd_kl_problem* prob, const uint16_t* H, const uin
   DeviceInfo di;
   if ((st = device_info(&di)) != KD_OK) return st;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  forget_forward(workspace);
   int* status = at<int>(workspace, 0);
   KD_CUDA(cudaMemsetAsync(workspace, 0, kHeaderBytes, stream));
   if (prob->T == 0) {
@@ -1211,6 +1219,7 @@ kd_status kd_rkl_backward(const kd_kl_problem* prob, const uint16_t* H, const ui
   DeviceInfo di;
   if ((st = device_info(&di)) != KD_OK) return st;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  forget_forward(workspace);
   int* status = at<int>(workspace, 0);
   KD_CUDA(cudaMemsetAsync(workspace, 0, kHeaderBytes, stream));
   if (prob->T == 0) {
@@ -1255,6 +1264,7 @@ kd_status kd_lmhead_topk(const kd_topk_problem* prob, const uint16_t* H, const u
   const TopkPlan f = plan_topk(p, di.num_sms, pair, procs);
   if (workspace_bytes < f.total) return KD_ERR_WORKSPACE;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  forget_forward(workspace);
   int* status = at<int>(workspace, 0);
   KD_CUDA(cudaMemsetAsync(workspace, 0, kHeaderBytes, stream));
   if (p.T == 0) return KD_OK;

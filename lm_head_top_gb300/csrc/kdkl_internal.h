@@ -272,5 +272,8 @@ cudaError_t launch_adamw(const AdamTensor* t, int n, int blocks, bool param_bf16
 
 // kdkl_api.cu: the current device's SM count; KD_OK, KD_ERR_CUDA or KD_ERR_UNSUPPORTED.
 int current_device(int* num_sms);
+// ... and what every call does with its workspace before it overwrites it: a record of a
+// KL forward whose teacher rows lie there is dropped, so that no backward reuses them.
+void forget_forward(const void* workspace);
 
 }  // namespace kdkl

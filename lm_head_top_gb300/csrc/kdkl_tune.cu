@@ -123,6 +123,7 @@ kd_status kd_policy_loss(const kd_policy_problem* prob, const float* logp, const
   int sms = 0;
   if ((st = (kd_status)current_device(&sms)) != KD_OK) return st;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  forget_forward(workspace);
   sms = std::min(sms, kMaxSms);
   // status, counts, ticket and the sequences' counts start at zero
   const size_t zeros = p.reduction == KD_REDUCE_SEQUENCE ? L.off_part : kHeader;
@@ -194,6 +195,7 @@ kd_status kd_pref_loss(const kd_pref_problem* prob, const float* logp, const flo
   int sms = 0;
   if ((st = (kd_status)current_device(&sms)) != KD_OK) return st;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  forget_forward(workspace);
   sms = std::min(sms, kMaxSms);
   if (p.P == 0) {
     if (cudaMemsetAsync(workspace, 0, kHeader, stream) != cudaSuccess) return KD_ERR_CUDA;
