@@ -357,7 +357,7 @@ enum { KD_REDUCE_TOKEN = 0, KD_REDUCE_SEQUENCE = 1, KD_REDUCE_SUM = 2 };
 
 typedef struct {
   int64_t T;         /* tokens, below 2^31 - 4096 */
-  int64_t S;         /* sequences; 0 without cu_seqlens */
+  int64_t S;         /* sequences, up to 2^30; 0 without cu_seqlens */
   double clip_low;   /* in [0, 1] */
   double clip_high;  /* >= 0 */
   double dual_clip;  /* > 1, or 0: off */
@@ -399,7 +399,7 @@ enum { KD_PREF_SIGMOID = 0, KD_PREF_IPO = 1, KD_PREF_HINGE = 2 };
 
 typedef struct {
   int64_t T;               /* tokens, below 2^31 - 4096 */
-  int64_t P;               /* pairs: 2 P sequences, 2 P < 2^31 - 1 */
+  int64_t P;               /* pairs: 2 P sequences, up to 2^30 */
   double beta;             /* > 0 */
   double label_smoothing;  /* in [0, 1) */
   double margin;

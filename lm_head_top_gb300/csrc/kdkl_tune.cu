@@ -15,6 +15,9 @@ constexpr size_t kHeader = 256;  // int status; two counts; a ticket
 // Bound on the SM count that sizes workspaces (the same with and without a device).
 constexpr int kMaxSms = 256;
 constexpr int64_t kMaxTokens = (1ll << 31) - 4096;  // a block's token indexes stay in 31 bits
+// The searches among the sequences double a step of at most S, and round S up to 32s: in
+// 31 bits up to here.
+constexpr int64_t kMaxSequences = 1ll << 30;
 
 inline size_t pad256(size_t x) { return (x + 255) & ~(size_t)255; }
 inline bool aligned_to(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -51,7 +54,7 @@ PolicyLayout policy_layout(const kd_policy_problem& p) {
 
 kd_status policy_check(const kd_policy_problem* p) {
   if (!p) return KD_ERR_INVALID_ARG;
-  if (p->T < 0 || p->T >= kMaxTokens || p->S < 0 || p->S >= (1ll << 31) - 1) return KD_ERR_SHAPE;
+  if (p->T < 0 || p->T >= kMaxTokens || p->S < 0 || p->S > kMaxSequences) return KD_ERR_SHAPE;
   if (!(p->clip_low >= 0.0 && p->clip_low <= 1.0) || !(p->clip_high >= 0.0))
     return KD_ERR_INVALID_ARG;
   if (!(p->dual_clip == 0.0 || p->dual_clip > 1.0) || !isfinite(p->dual_clip))
@@ -81,7 +84,7 @@ PrefLayout pref_layout(const kd_pref_problem& p) {
 
 kd_status pref_check(const kd_pref_problem* p) {
   if (!p) return KD_ERR_INVALID_ARG;
-  if (p->T < 0 || p->T >= kMaxTokens || p->P < 0 || p->P >= (1ll << 30) - 1) return KD_ERR_SHAPE;
+  if (p->T < 0 || p->T >= kMaxTokens || p->P < 0 || p->P > kMaxSequences / 2) return KD_ERR_SHAPE;
   if (p->T > 0 && p->P < 1) return KD_ERR_SHAPE;
   if (!(p->beta > 0.0) || !isfinite(p->beta) || !isfinite(p->margin)) return KD_ERR_INVALID_ARG;
   if (!(p->label_smoothing >= 0.0 && p->label_smoothing < 1.0)) return KD_ERR_INVALID_ARG;
