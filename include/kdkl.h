@@ -361,8 +361,8 @@ typedef struct {
   double clip_low;   /* in [0, 1] */
   double clip_high;  /* >= 0 */
   double dual_clip;  /* > 1, or 0: off */
-  double kl_coef;    /* finite; 0 without ref_logp */
-  double norm;       /* KD_REDUCE_SUM: > 0 */
+  double kl_coef;    /* finite in 32 bits; 0 without ref_logp */
+  double norm;       /* KD_REDUCE_SUM: > 0, and 1 / norm finite in 32 bits */
   int32_t reduction;
   int32_t advantage_per_sequence; /* advantages are [S], else [T] */
 } kd_policy_problem;
@@ -377,7 +377,7 @@ size_t kd_policy_workspace_size(const kd_policy_problem* prob);
  *               never falling (empty sequences allowed); needed, and read, for
  *               KD_REDUCE_SEQUENCE and advantages per sequence only.
  *               Otherwise KD_ERR_INVALID_ARG through kd_kl_check_status
- *   grad_loss   upstream gradient (host scalar)
+ *   grad_loss   upstream gradient (host scalar), and grad_loss / norm finite in 32 bits
  *   loss        [1] fp32 out (0 when nothing counts)
  *   stats       [3] fp32 out or NULL   sum w (-s), sum w k, share of counted tokens clipped
  *   grad_logp   [T] fp32 out or NULL   grad_loss * dloss/dlogp (0 where not counted)
@@ -400,7 +400,7 @@ enum { KD_PREF_SIGMOID = 0, KD_PREF_IPO = 1, KD_PREF_HINGE = 2 };
 typedef struct {
   int64_t T;               /* tokens, below 2^31 - 4096 */
   int64_t P;               /* pairs: 2 P sequences, up to 2^30 */
-  double beta;             /* > 0 */
+  double beta;             /* > 0, in 32 bits too; 1 / (2 beta) and margin finite there */
   double label_smoothing;  /* in [0, 1) */
   double margin;
   int32_t kind;

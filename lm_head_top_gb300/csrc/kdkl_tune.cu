@@ -34,6 +34,10 @@ bool vectors(const void* a, const void* b, const void* c, const void* d, const v
          aligned_to(e, 16) && aligned_to(mask, 16);
 }
 
+// Finite as the kernels take it. (An infinite weight times the zero of a token that is
+// not counted would be a NaN.)
+bool fits32(double x) { return isfinite((float)x); }
+
 // A border in 48 bits: the nearest float and the remainder.
 void split_border(double x, float* hi, float* lo) {
   *hi = (float)x;
@@ -59,9 +63,10 @@ kd_status policy_check(const kd_policy_problem* p) {
     return KD_ERR_INVALID_ARG;
   if (!(p->dual_clip == 0.0 || p->dual_clip > 1.0) || !isfinite(p->dual_clip))
     return KD_ERR_INVALID_ARG;
-  if (!isfinite(p->kl_coef)) return KD_ERR_INVALID_ARG;
+  if (!fits32(p->kl_coef)) return KD_ERR_INVALID_ARG;
   if (p->reduction < KD_REDUCE_TOKEN || p->reduction > KD_REDUCE_SUM) return KD_ERR_INVALID_ARG;
-  if (p->reduction == KD_REDUCE_SUM && !(p->norm > 0.0 && isfinite(p->norm)))
+  if (p->reduction == KD_REDUCE_SUM &&
+      !(p->norm > 0.0 && isfinite(p->norm) && fits32(1.0 / p->norm)))
     return KD_ERR_INVALID_ARG;
   if ((p->reduction == KD_REDUCE_SEQUENCE || p->advantage_per_sequence) && p->T > 0 && p->S < 1)
     return KD_ERR_SHAPE;
@@ -86,7 +91,8 @@ kd_status pref_check(const kd_pref_problem* p) {
   if (!p) return KD_ERR_INVALID_ARG;
   if (p->T < 0 || p->T >= kMaxTokens || p->P < 0 || p->P > kMaxSequences / 2) return KD_ERR_SHAPE;
   if (p->T > 0 && p->P < 1) return KD_ERR_SHAPE;
-  if (!(p->beta > 0.0) || !isfinite(p->beta) || !isfinite(p->margin)) return KD_ERR_INVALID_ARG;
+  if (!((float)p->beta > 0.f) || !fits32(p->beta) || !fits32(0.5 / p->beta) || !fits32(p->margin))
+    return KD_ERR_INVALID_ARG;
   if (!(p->label_smoothing >= 0.0 && p->label_smoothing < 1.0)) return KD_ERR_INVALID_ARG;
   if (p->kind < KD_PREF_SIGMOID || p->kind > KD_PREF_HINGE) return KD_ERR_INVALID_ARG;
   return KD_OK;
@@ -116,7 +122,9 @@ kd_status kd_policy_loss(const kd_policy_problem* prob, const float* logp, const
   const bool per_seq = p.reduction == KD_REDUCE_SEQUENCE || p.advantage_per_sequence;
   if (per_seq && p.T > 0 && !cu_seqlens) return KD_ERR_INVALID_ARG;
   if (!ref_logp && p.kl_coef != 0.0 && p.T > 0) return KD_ERR_INVALID_ARG;
-  if (!isfinite(grad_loss)) return KD_ERR_INVALID_ARG;
+  if (!isfinite(grad_loss) ||
+      (p.reduction == KD_REDUCE_SUM && !fits32((double)grad_loss / p.norm)))
+    return KD_ERR_INVALID_ARG;
   if (!aligned_to(logp, 4) || !aligned_to(old_logp, 4) || !aligned_to(ref_logp, 4) ||
       !aligned_to(advantages, 4) || !aligned_to(cu_seqlens, 4) || !aligned_to(loss, 4) ||
       !aligned_to(stats, 4) || !aligned_to(grad_logp, 4) || !aligned_to(workspace, 16))
