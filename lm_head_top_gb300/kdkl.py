@@ -708,16 +708,19 @@ def kd_pref_loss(logp, ref_logp, cu_seqlens, mask=None, *, beta=0.1, kind="sigmo
 
 class KDAdamWTensors:
     """The tensors of an AdamW step, checked once: the host table that kd_adamw_step
-    passes to the library, and the tensors it points to (kept alive, not copied)."""
+    passes to the library, and the memory it points to (kept alive, not copied, also when
+    a list or a tensor's data is exchanged). A step works on that memory: it does not
+    notice that a gradient has been replaced since, and takes the old one."""
 
-    def __init__(self, table, n, device, tensors, param_bf16, grad_bf16, state_8bit):
-        self.table, self.n, self.device, self.tensors = table, n, device, tensors
+    def __init__(self, table, n, device, memory, param_bf16, grad_bf16, state_8bit):
+        self.table, self.n, self.device, self.memory = table, n, device, memory
         self.param_bf16, self.grad_bf16, self.state_8bit = param_bf16, grad_bf16, state_8bit
 
 
 def kd_adamw_tensors(params, grads, exp_avg, exp_avg_sq, *, copies=None, m_scales=None,
                      v_scales=None, decay=None) -> KDAdamWTensors:
-    """The list of tensors for kd_adamw_step; make it again when a tensor is replaced.
+    """The list of tensors for kd_adamw_step; make it again when a tensor is replaced (a
+    step cannot notice: gradients are new tensors after ``zero_grad(set_to_none=True)``).
 
     params: fp32 or bf16; grads: fp32 or bf16. exp_avg / exp_avg_sq: fp32 (m and v), or
     torch.float8_e4m3fn (m and sqrt(v)) with ``m_scales`` / ``v_scales``: fp32, one for
@@ -733,7 +736,7 @@ def kd_adamw_tensors(params, grads, exp_avg, exp_avg_sq, *, copies=None, m_scale
     if decay is not None and len(decay) != n:
         raise ValueError("decay has %d values, expected %d" % (len(decay), n))
     if n == 0:
-        return KDAdamWTensors((kd_adamw_tensor * 1)(), 0, None, lists, 0, 0, 0)
+        return KDAdamWTensors((kd_adamw_tensor * 1)(), 0, None, [], 0, 0, 0)
     dev = params[0].device
     p_t, g_t, s_t = params[0].dtype, grads[0].dtype, exp_avg[0].dtype
     if p_t not in (torch.float32, torch.bfloat16):
@@ -745,7 +748,7 @@ def kd_adamw_tensors(params, grads, exp_avg, exp_avg_sq, *, copies=None, m_scale
     s8 = s_t == torch.float8_e4m3fn
     if s8 and (m_scales is None or v_scales is None):
         raise ValueError("8-bit states need m_scales and v_scales")
-    table = (kd_adamw_tensor * n)()
+    table, memory = (kd_adamw_tensor * n)(), []
     for i in range(n):
         shape, count = tuple(params[i].shape), params[i].numel()
         blocks = (count + KD_ADAMW_BLOCK - 1) // KD_ADAMW_BLOCK
@@ -768,9 +771,10 @@ def kd_adamw_tensors(params, grads, exp_avg, exp_avg_sq, *, copies=None, m_scale
                     raise ValueError("%s of tensor %d is on %s, expected %s"
                                      % (field, i, ts[i].device, dev))
                 setattr(row, field, ts[i].data_ptr())
+                memory.append(ts[i].untyped_storage())
         row.n = count
         row.decay = 1 if decay is None or decay[i] else 0
-    return KDAdamWTensors(table, n, dev, lists, 1 if p_t == torch.bfloat16 else 0,
+    return KDAdamWTensors(table, n, dev, memory, 1 if p_t == torch.bfloat16 else 0,
                           1 if g_t == torch.bfloat16 else 0, 1 if s8 else 0)
 
 
