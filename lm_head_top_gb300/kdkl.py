@@ -783,12 +783,13 @@ def kd_adamw_step(tensors: KDAdamWTensors, *, lr, betas=(0.9, 0.999), eps=1e-8, 
     """One AdamW step, in place, on the tensors of kd_adamw_tensors. ``step`` counts from 1.
     The gradients are multiplied by ``grad_scale`` and, if given, by the device scalar
     ``grad_scale_dev`` ([1] fp32, a clip coefficient)."""
+    if not tensors.n:
+        return
     o = kd_adamw_options(lr, betas[0], betas[1], eps, weight_decay, int(step),
                          _addr(grad_scale_dev, "grad_scale_dev", torch.float32, (1,),
                                tensors.device),
                          grad_scale, tensors.param_bf16, tensors.grad_bf16, tensors.state_8bit)
-    if tensors.n:
-        _launch("kd_adamw_step", tensors.device, stream, tensors.table, tensors.n, ctypes.byref(o))
+    _launch("kd_adamw_step", tensors.device, stream, tensors.table, tensors.n, ctypes.byref(o))
 
 
 def kd_kl_check_status(workspace: torch.Tensor, stream=None) -> int:
