@@ -740,7 +740,8 @@ __global__ void __launch_bounds__(256)
 // Per token, the vocabulary splits' partials (max, sum of exponentials, the
 // logit at the token's id) to lse and logp = (z - max)/tau - log(sum): the
 // maximum cancels before it is scaled. The tensor core's sum of d products loses
-// digits (1e-6 of a logit at d = 2880) that the token's own logit, often the
+// digits (1e-6 of a logit at d = 2880, 1e-5 if all products have one sign) that the
+// token's own logit, often the
 // largest of its row, hands on to logp and lse in full; zdot has it in fp32 sums,
 // and its share of the sum of exponentials is corrected with it:
 // log(S + e^z' - e^z) = log S + log(1 + p (e^(z'-z) - 1)), p = e^z / S.
