@@ -676,8 +676,8 @@ __global__ void __launch_bounds__(SCAN_THREADS)
 }
 
 // A row per counted token, a warp each: the token's id with weight 1 as a
-// teacher row of one entry, so that the GEMM epilogues pick z at that id and
-// subtract its one-hot; with Hc, the token's row of H copied there (rows from N
+// teacher row of one entry, so that the GEMM epilogues pick z at that id (the
+// forward) or leave its gradient to what is added later (the backward); with Hc, the token's row of H copied there (rows from N
 // to the end of N's last tile of `round` are zeroed); the id's logit before scaling,
 // H row . W row in fp32 (a lane's products, then a tree): into zdot, or (zdot null)
 // with the token's lse and gradient the coefficient of the row's own terms,
@@ -741,9 +741,8 @@ __global__ void __launch_bounds__(256)
 // logit at the token's id) to lse and logp = (z - max)/tau - log(sum): the
 // maximum cancels before it is scaled. The tensor core's sum of d products loses
 // digits (1e-6 of a logit at d = 2880, 1e-5 if all products have one sign) that the
-// token's own logit, often the
-// largest of its row, hands on to logp and lse in full; zdot has it in fp32 sums,
-// and its share of the sum of exponentials is corrected with it:
+// token's own logit, often the largest of its row, hands on to logp and lse in full;
+// zdot has it in fp32 sums, and its share of the sum of exponentials is corrected with it:
 // log(S + e^z' - e^z) = log S + log(1 + p (e^(z'-z) - 1)), p = e^z / S.
 // TOK tokens per block, 256 / TOK threads on each one's splits, merged in a
 // fixed order. invmap as in lse_combine.

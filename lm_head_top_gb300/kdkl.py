@@ -594,7 +594,9 @@ def kd_logprob_backward(H, W, ids, lse, grad_logp, *, temperature=1.0, chunk=409
                         stream=None):
     """Gradients of sum_t grad_logp[t] * logp[t]. Returns (dH [T,d] bf16, dW [V,d] in
     ``dW_dtype``: fp32, which may be added to, or bf16). Tokens whose gradient is
-    zero are skipped."""
+    zero are skipped. ``chunk`` bounds the workspace: chunk * V bf16 values of the
+    gradient of the logits at a time, 1.6 GB at the default and V = 201,088. At 1024 it is
+    a quarter of that and the call 3 % slower (6.77 and 6.59 ms for 3000 tokens)."""
     T, d, V, dev, operands = _logprob_args(H, W, ids)
     given = (_addr(lse, "lse", torch.float32, (T,), dev),
              _addr(grad_logp, "grad_logp", torch.float32, (T,), dev))
