@@ -751,29 +751,26 @@ def kd_adamw_tensors(params, grads, exp_avg, exp_avg_sq, *, copies=None, m_scale
     if s8 and (m_scales is None or v_scales is None):
         raise ValueError("8-bit states need m_scales and v_scales")
     table, memory = (kd_adamw_tensor * n)(), []
+    columns = [c for c in (("param", "params", params, p_t), ("grad", "grads", grads, g_t),
+                           ("exp_avg", "exp_avg", exp_avg, s_t),
+                           ("exp_avg_sq", "exp_avg_sq", exp_avg_sq, s_t),
+                           ("copy", "copies", copies, torch.bfloat16),
+                           ("m_scale", "m_scales", m_scales if s8 else None, torch.float32),
+                           ("v_scale", "v_scales", v_scales if s8 else None, torch.float32))
+               if c[2] is not None]
     for i in range(n):
-        shape, count = tuple(params[i].shape), params[i].numel()
+        shape, count = params[i].shape, params[i].numel()
         blocks = (count + KD_ADAMW_BLOCK - 1) // KD_ADAMW_BLOCK
-        _check(params[i], "params[%d]" % i, p_t, shape)
-        _check(grads[i], "grads[%d]" % i, g_t, shape)
-        _check(exp_avg[i], "exp_avg[%d]" % i, s_t, shape)
-        _check(exp_avg_sq[i], "exp_avg_sq[%d]" % i, s_t, shape)
-        if copies is not None:
-            _check(copies[i], "copies[%d]" % i, torch.bfloat16, shape)
-        if s8:
-            _check(m_scales[i], "m_scales[%d]" % i, torch.float32, (blocks,))
-            _check(v_scales[i], "v_scales[%d]" % i, torch.float32, (blocks,))
         row = table[i]
-        for field, ts in (("param", params), ("grad", grads), ("exp_avg", exp_avg),
-                          ("exp_avg_sq", exp_avg_sq), ("copy", copies),
-                          ("m_scale", m_scales if s8 else None),
-                          ("v_scale", v_scales if s8 else None)):
-            if ts is not None:
-                if ts[i].device != dev:
-                    raise ValueError("%s of tensor %d is on %s, expected %s"
-                                     % (field, i, ts[i].device, dev))
-                setattr(row, field, ts[i].data_ptr())
-                memory.append(ts[i].untyped_storage())
+        for field, name, ts, dtype in columns:
+            t = ts[i]
+            want = shape if field[1:] != "_scale" else (blocks,)
+            if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == want
+                    and t.device == dev and t.is_cuda and t.is_contiguous()):
+                _check(t, "%s[%d]" % (name, i), dtype, want)
+                raise ValueError("%s of tensor %d is on %s, expected %s" % (field, i, t.device, dev))
+            setattr(row, field, t.data_ptr())
+            memory.append(t.untyped_storage())
         row.n = count
         row.decay = 1 if decay is None or decay[i] else 0
     return KDAdamWTensors(table, n, dev, memory, 1 if p_t == torch.bfloat16 else 0,
