@@ -871,11 +871,10 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
           th = topk_shared_threshold(rkey);
         }
       }
-      float* side_row = nullptr;  // EPI_STORE: see EpiParams::side
-      if (EPI == EPI_STORE && eo.first_row && r < eo.out_rows) {
-        const int left = eo.first_row[r];
-        if (left) side_row = eo.side + (long long)(eo.T - left) * eo.ldo;
-      }
+      // EPI_STORE: see EpiParams::side. Not looked at before the accumulator is there: the
+      // wait for it hides this load's.
+      int side_left = 0;
+      if (EPI == EPI_STORE && eo.first_row && r < eo.out_rows) side_left = eo.first_row[r];
       // MIX row state: temperature-1 sum, label logit, label id
       float run_s1 = 0.f, zl = 0.f, lse12 = 0.f, w_kl = 0.f, w_ce = 0.f;
       int lab = -1;
@@ -1074,12 +1073,14 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
           } else {  // EPI_STORE
             const int r0 = r - lane;
             if (eo.out16) {
-              if (side_row) {  // few rows have own terms
+              if (side_left) {  // few rows have own terms
+                float4* to = reinterpret_cast<float4*>(
+                    eo.side + (long long)(eo.T - side_left) * eo.ldo + cl);
+                const int quads = (eo.out_cols - cl) >> 2;  // 8 but at the end of a row
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                  if (cl + 4 * j < eo.out_cols)
-                    *reinterpret_cast<float4*>(side_row + cl + 4 * j) =
-                        make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                  if (quads >= 8 || j < quads)
+                    to[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
               }
               stage_bf16(v, 4 * (c & 1));
               if ((c & 1) || cl + 32 >= eo.out_cols) {
