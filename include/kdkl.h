@@ -298,7 +298,8 @@ kd_status kd_lmhead_topk(const kd_topk_problem* prob, const uint16_t* H, const u
  * optimizer's step. As above: device pointers, no allocation, asynchronous on
  * `stream`, device-detected errors through kd_kl_check_status(workspace).
  *
- * Token log-probabilities of the LM head, the logits never stored:
+ * Token log-probabilities of the LM head, the logits never stored (the backward holds
+ * the gradient of up to chunk * V of them at a time):
  *   z = H W^T / tau,  lse[t] = log sum_v exp(z[t,v]),  logp[t] = z[t,ids[t]] - lse[t]
  *   dL/dz[t,v] = g[t] (onehot(ids[t])[v] - softmax(z[t])[v]),  g = dL/dlogp
  *   dH = dL/dz . W / tau,  dW = (dL/dz)^T . H / tau */
