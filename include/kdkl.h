@@ -389,6 +389,7 @@ size_t kd_policy_workspace_size(const kd_policy_problem* prob);
  *               one for A >= 0 (a token of advantage 0 too, though nothing depends on its
  *               ratio), the lower one or the dual one for A < 0
  *   grad_logp   [T] fp32 out or NULL   grad_loss * dloss/dlogp (0 where not counted)
+ * Ratios and penalties are formed in fp32 (e^x to 2 ulp and 2^-24 |x|), sums in 48 bits.
  * Sums have a fixed order: results are the same from run to run. */
 kd_status kd_policy_loss(const kd_policy_problem* prob, const float* logp, const float* old_logp,
                          const float* ref_logp, const float* advantages, const uint8_t* mask,
