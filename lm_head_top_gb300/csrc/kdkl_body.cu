@@ -127,7 +127,7 @@ struct RoundPlan {
   MuonGroup g[MUON_GROUPS];
   size_t off[MUON_GROUPS], x_bytes[MUON_GROUPS], s_bytes[MUON_GROUPS];  // of a matrix
   int64_t rows[MUON_GROUPS], cols[MUON_GROUPS];
-  size_t total;
+  size_t off_piece, total;
 };
 
 int round64(int64_t x) { return (int)((x + 63) / 64 * 64); }
@@ -179,7 +179,8 @@ void plan_round(const kd_muon_matrix* m, int n, int begin, size_t full, RoundPla
   p.end = i;
   size_t o = kHeader, parts = 0;
   for (int g = 0; g < p.n_groups; ++g) parts += (size_t)p.g[g].parts * p.g[g].count;
-  o += pad256(parts * 4);
+  p.off_piece = o + pad256(parts * sizeof(float));
+  o = p.off_piece + pad256(parts * sizeof(float2));
   for (int g = 0; g < p.n_groups; ++g) {
     p.off[g] = o;
     o += 2 * pad256(p.x_bytes[g] * p.g[g].count) + 2 * pad256(p.s_bytes[g] * p.g[g].count);
@@ -267,6 +268,7 @@ kd_status muon_round(const kd_muon_matrix* m, int begin, RoundPlan& p, const kd_
   r.grad_scale_dev = o.grad_scale_dev;
   r.nesterov = o.nesterov != 0;
   r.part = place<float>(ws, kHeader);
+  r.piece = place<float2>(ws, p.off_piece);
   // the groups with the longest products first: their tiles are handed out in this order
   int order[MUON_GROUPS];
   for (int g = 0; g < p.n_groups; ++g) {

@@ -89,7 +89,8 @@ struct MuonRound {
   float momentum, eps, grad_scale;
   int nesterov;
   const float* grad_scale_dev;
-  float* part;  // sums of squares
+  float* part;    // sums of squares by pieces, or -inf: see `piece`
+  float2* piece;  // sums of squares of u / unit, and the unit
 };
 struct MuonList {
   MuonMatrix m[MUON_LIST];

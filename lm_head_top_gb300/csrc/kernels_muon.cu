@@ -26,6 +26,10 @@
 // product needs one, it copies the one across the diagonal and has the tensor core read it
 // the other way (MN-major instead of K-major).
 //
+// |u| is that of u at any size: squares of fp32 vanish below 2^-75 and overflow above 2^64, so
+// where a piece's largest magnitude is beyond 2^-40 or 2^40 its squares are taken again, of u by a
+// power of two (SquareSum).
+//
 // What bounds it: the tensor cores, from r of about 1000 on. Work: 3 (r r k + r^3 +
 // 2 r r k) flops a step, the 3 for the halves.
 //
@@ -120,6 +124,71 @@ __device__ __forceinline__ float block_sum(float v) {
   return s;
 }
 
+// A sum of squares of u / unit. The unit is 1 where the largest magnitude is within 2^-40 and 2^40
+// (squares of 2^32 elements stay below 2^112, and what is lost below 2^-63 of them is nothing beside
+// it), else 2^84 or 2^-84, which bring all that lies beyond within 2^-65 and 2^44.
+constexpr float U_LARGE = 0x1p40f, U_SMALL = 0x1p-40f, U_UNIT = 0x1p84f;
+
+struct SquareSum {
+  float sum = 0.f, most = 0.f;
+  __device__ __forceinline__ void add(float u) {
+    sum += u * u;
+    most = fmaxf(most, fabsf(u));
+  }
+  // Of the block's: the sum, and the unit that it ought to have been taken in (a NaN is in the sum,
+  // if not in the maximum).
+  template <int THREADS>
+  __device__ __forceinline__ float over_block() {
+    __shared__ float2 red[THREADS / 32];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    }
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(sum, most);
+    __syncthreads();
+    sum = most = 0.f;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+      sum += red[w].x;
+      most = fmaxf(most, red[w].y);
+    }
+    return most > U_LARGE ? U_UNIT : most > 0.f && most < U_SMALL ? 1.f / U_UNIT : 1.f;
+  }
+};
+
+// The sum of a matrix's pieces where one of them is not in 1's, and the largest unit that there is,
+// which it is in.
+// (A call of its own: its registers would be a thread block less on an SM for the layout pass.)
+__device__ __noinline__ float2 sum_of_units(const float2* piece, int pieces) {
+  float ss = 0.f, large = 0.f, small = 0.f;
+  for (int i = threadIdx.x; i < pieces; i += EW_THREADS) {
+    const float2 p = piece[i];
+    if (p.y == 1.f)
+      ss += p.x;
+    else if (p.y > 1.f)
+      large += p.x;
+    else
+      small += p.x;
+  }
+  ss = block_sum<EW_THREADS>(ss);
+  large = block_sum<EW_THREADS>(large);
+  small = block_sum<EW_THREADS>(small);
+  auto in_next = [](float sum) { return sum * (1.f / U_UNIT) * (1.f / U_UNIT); };
+  if (!(large == 0.f)) return make_float2(large + in_next(ss + in_next(small)), U_UNIT);
+  if (!(ss == 0.f)) return make_float2(ss + in_next(small), 1.f);
+  return make_float2(small, 1.f / U_UNIT);
+}
+
+// What u is multiplied by to be X times 2^13: by max(|u|, eps), where u's squares over the unit's
+// add up to ss (NaN stays NaN). Normal up to |u| = 2^139; at the most that a matrix can have, 2^144,
+// it holds 18 bits.
+__device__ __forceinline__ float to_x(float ss, float unit, float eps) {
+  const float norm = sqrtf(ss), least = eps / unit;
+  return X_SCALE / (norm < least ? least : norm) / unit;
+}
+
 // The group that number `x` of a launch falls in; `start` gives each group's first.
 template <typename F>
 __device__ __forceinline__ int group_of(const MuonRound& r, int x, F start) {
@@ -142,12 +211,11 @@ __global__ void __launch_bounds__(EW_THREADS)
   const float mu = r.momentum;
   grid_dependency_wait();
   const float s = r.grad_scale_dev ? r.grad_scale * *r.grad_scale_dev : r.grad_scale;
-  float ss = 0.f;
+  SquareSum squares;
   auto one = [&](float grad, float& mom) {
     const float gs = __fmul_rn(grad, s);
     mom = new_momentum(mom, mu, gs);
-    const float u = r.nesterov ? new_momentum(mom, mu, gs) : mom;
-    ss += u * u;
+    squares.add(r.nesterov ? new_momentum(mom, mu, gs) : mom);
   };
   long long i = begin;
   if (((uintptr_t)m.momentum & 15) == 0 && ((uintptr_t)m.grad & 15) == 0) {
@@ -165,8 +233,22 @@ __global__ void __launch_bounds__(EW_THREADS)
     i = whole;
   }
   for (i += threadIdx.x; i < end; i += EW_THREADS) one(load_grad<G>(m.grad, i), m.momentum[i]);
-  ss = block_sum<EW_THREADS>(ss);
-  if (threadIdx.x == 0) r.part[g.part0 + local] = ss;
+  const float unit = squares.over_block<EW_THREADS>();
+  float ss = squares.sum;
+  if (unit != 1.f) {  // all of the block: from what it has written
+    ss = 0.f;
+    for (i = begin + threadIdx.x; i < end; i += EW_THREADS) {
+      const float mom = m.momentum[i];
+      float u = r.nesterov ? new_momentum(mom, mu, __fmul_rn(load_grad<G>(m.grad, i), s)) : mom;
+      u *= 1.f / unit;
+      ss += u * u;
+    }
+    ss = block_sum<EW_THREADS>(ss);
+  }
+  if (threadIdx.x == 0) {
+    r.part[g.part0 + local] = unit == 1.f ? ss : -INFINITY;
+    r.piece[g.part0 + local] = make_float2(ss, unit);
+  }
 }
 
 // x as two halves.
@@ -199,10 +281,12 @@ __global__ void __launch_bounds__(EW_THREADS)
   const int row0 = local / tc * MUON_TILE, col0 = (local - local / tc * tc) * MUON_TILE;
   const MuonMatrix& m = l.m[g.first + which];
   grid_dependency_wait();
-  float ss = 0.f;
-  for (int i = threadIdx.x; i < g.parts; i += EW_THREADS) ss += r.part[g.part0 + which * g.parts + i];
-  const float norm = sqrtf(block_sum<EW_THREADS>(ss));
-  const float to = X_SCALE / (norm < r.eps ? r.eps : norm);  // NaN stays NaN
+  const int part0 = g.part0 + which * g.parts;
+  float2 sum = make_float2(0.f, 1.f);  // and its unit
+  for (int i = threadIdx.x; i < g.parts; i += EW_THREADS) sum.x += r.part[part0 + i];
+  sum.x = block_sum<EW_THREADS>(sum.x);
+  if (!(sum.x >= 0.f)) sum = sum_of_units(r.piece + part0, g.parts);
+  const float to = to_x(sum.x, sum.y, r.eps);
   const float s = r.grad_scale_dev ? r.grad_scale * *r.grad_scale_dev : r.grad_scale;
   __half* hi = g.X[0] + (long long)which * 2 * g.r * g.ldk;
   __half* lo = hi + (long long)g.r * g.ldk;
@@ -838,7 +922,7 @@ __global__ void __launch_bounds__(SMALL_THREADS, 1)
   auto index = [&](const Place& p) { return p.row * cols + p.col; };
   const Place start{warp, lane};
   // momentum, and the sum of squares
-  float ss = 0.f;
+  SquareSum squares;
   Place at = start;
 #pragma unroll 1
   for (int b = 0; b < places; b += SMALL_BATCH) {
@@ -854,12 +938,22 @@ __global__ void __launch_bounds__(SMALL_THREADS, 1)
       const float gs = __fmul_rn(gr[j], s);
       mom[j] = new_momentum(mom[j], a.momentum, gs);
       if (in(at)) m.momentum[index(at)] = mom[j];
-      const float u = a.nesterov ? new_momentum(mom[j], a.momentum, gs) : mom[j];
-      ss += u * u;
+      squares.add(a.nesterov ? new_momentum(mom[j], a.momentum, gs) : mom[j]);
     }
   }
-  const float norm = sqrtf(block_sum<SMALL_THREADS>(ss));  // (X's zeros are there)
-  const float to = X_SCALE / (norm < a.eps ? a.eps : norm);  // NaN stays NaN
+  const float unit = squares.over_block<SMALL_THREADS>();  // (X's zeros are there)
+  float ss = squares.sum;
+  if (unit != 1.f) {  // all of the block: from what it has written
+    ss = 0.f;
+    for (int i = threadIdx.x; i < rows * cols; i += SMALL_THREADS) {
+      const float mom = m.momentum[i];
+      float u = a.nesterov ? new_momentum(mom, a.momentum, __fmul_rn(load_grad<G>(m.grad, i), s)) : mom;
+      u *= 1.f / unit;
+      ss += u * u;
+    }
+    ss = block_sum<SMALL_THREADS>(ss);
+  }
+  const float to = to_x(ss, unit, a.eps);
   auto x_of = [&](const Place& p) {
     const int row = tall ? p.col : p.row, col = tall ? p.row : p.col;
     return small_piece(X + (col >> 6) * SMALL_BLOCK, row, (col & 63) >> 3) + (col & 7) * 2;
