@@ -532,7 +532,8 @@ typedef struct {
 
 /*   x, residual  [T, d]       residual NULL: h is x, and the argument h is not written
  *   weight, bias [d]          NULL: 1 and 0
- *   y            [T, d] out   may be x or residual
+ *   y            [T, d] out   may be x (which, without a residual, the backward needs) or
+ *                             residual
  *   h            [T, d] out   needed with residual; may be x or residual, not y
  *   mean         [T] fp32 out or NULL   KD_NORM_LAYER only
  *   rstd         [T] fp32 out or NULL */

@@ -928,7 +928,9 @@ def kd_norm_forward(x, weight=None, bias=None, *, residual=None, kind="rms", eps
 
     x, residual: [T,d], fp32 or bf16; weight, bias (layer norm only): [d], fp32 or bf16.
     Returns (y [T,d], h [T,d], mean [T] fp32 or None for RMS, rstd [T] fp32): h is the sum,
-    rounded to x's type, and x itself without a residual. What kd_norm_backward takes."""
+    rounded to x's type, and x itself without a residual. What kd_norm_backward takes.
+    y may be x or residual, h may be x or residual: where y takes x's place and there is no
+    residual, what was normed is gone, and None is returned for h."""
     T, d, p = _norm_problem(x, weight, bias, kind, eps)
     dev, dtype = x.device, x.dtype
     wtype = None if weight is None and bias is None else (bias if weight is None else weight).dtype
@@ -944,9 +946,12 @@ def kd_norm_forward(x, weight=None, bias=None, *, residual=None, kind="rms", eps
     if kind == "layer":
         mean = _outcome(mean, "mean", torch.float32, (T,), dev, stream)
     rstd = _outcome(rstd, "rstd", torch.float32, (T,), dev, stream)
-    _launch("kd_norm_forward", dev, stream, ctypes.byref(p), *given, y.data_ptr(),
+    at = y.data_ptr()
+    _launch("kd_norm_forward", dev, stream, ctypes.byref(p), *given, at,
             None if h is None else h.data_ptr(), None if mean is None else mean.data_ptr(),
             rstd.data_ptr())
+    if h is None and (y is x or T > 0 and at == given[0]):
+        return y, None, mean, rstd
     return y, x if h is None else h, mean, rstd
 
 
