@@ -508,49 +508,50 @@ int backward_most(const RowPlan& p, int T, int num_sms) {
   return std::min(per_sm * num_sms, std::max(2 * num_sms, T / rows));
 }
 
-// What an SM holds of a kernel's blocks at once, which a grid is a multiple of (a last
-// block that waits for the others to end would be a round of its own). Asked for once for a
-// number of threads, on which the shared memory depends; concurrent first calls find the same.
+// What is found once for a kernel and device (concurrent first calls find the same): that it may
+// have more than 48 KB of shared memory, and, by a block's threads, on which the shared memory
+// depends, how many blocks an SM holds at once.
+struct KernelFacts {
+  std::atomic<bool> allowed;
+  std::atomic<int> blocks[33];
+};
+
+// Blocks that an SM holds, which a grid is a multiple of (a last block that waits for the others to
+// end would be a round of its own).
 template <typename K>
-cudaError_t resident(K kern, std::atomic<int>* known, int threads, int smem, int* blocks) {
-  std::atomic<int>& k = known[threads / 32];
+cudaError_t resident(K kern, KernelFacts* facts, int threads, int smem, int* blocks) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  KernelFacts& f = facts[dev];
+  if (!f.allowed.load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, NORM_BLOCK_SMEM);
+    if (e != cudaSuccess) return e;
+    f.allowed.store(true, std::memory_order_release);
+  }
+  std::atomic<int>& k = f.blocks[threads / 32];
   *blocks = k.load(std::memory_order_acquire);
   if (*blocks > 0) return cudaSuccess;
   int n = 0;
-  const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, smem);
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, smem);
   if (e != cudaSuccess) return e;
   *blocks = std::max(1, std::min(n, NORM_MAX_PER_SM));
   k.store(*blocks, std::memory_order_release);
   return cudaSuccess;
 }
 
-// More than 48 KB of shared memory a block has to be asked for, once for a kernel and device
-// (concurrent first calls ask for the same).
-template <typename K>
-cudaError_t allow_smem(K kern, std::atomic<bool>* done) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, NORM_BLOCK_SMEM);
-  if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
-  return e;
-}
-
 template <typename T, bool LAYER, int VEC, bool EDGES, int VPT, bool WARP, int THREADS>
 cudaError_t forward(const RowPlan& p, const NormArgs& a, int num_sms, cudaStream_t stream) {
   auto kern = norm_forward_kernel<T, LAYER, VEC, EDGES, VPT, WARP, THREADS>;
-  static std::atomic<bool> done[kMaxDevices] = {};
-  static std::atomic<int> known[33] = {};
+  static KernelFacts facts[kMaxDevices] = {};
   const int bytes = RowRing<T, VEC, EDGES, VPT, 2>::place_bytes(p.threads);
   const int places = ring_places(bytes, PLACES_FORWARD);
   const int w_bytes = (LAYER ? 2 : 1) * VPT * VEC * 4 * (WARP ? 32 : p.threads);
   const int w_smem = places * bytes + w_bytes <= NORM_BLOCK_SMEM;
   const int smem = places * bytes + (w_smem ? w_bytes : 0);
   int per_sm = 0;
-  cudaError_t e = allow_smem(kern, done);
-  if (e == cudaSuccess) e = resident(kern, known, p.threads, smem, &per_sm);
+  cudaError_t e = resident(kern, facts, p.threads, smem, &per_sm);
   if (e != cudaSuccess) return e;
   int most = per_sm * num_sms;
   if (!WARP) most = std::max(most, a.T / ROWS_FORWARD);
@@ -562,16 +563,14 @@ cudaError_t forward(const RowPlan& p, const NormArgs& a, int num_sms, cudaStream
 template <typename T, bool LAYER, int VEC, bool EDGES, int VPT, bool WARP, int THREADS>
 cudaError_t backward(const RowPlan& p, const NormArgs& a, int num_sms, cudaStream_t stream) {
   auto kern = norm_backward_kernel<T, LAYER, VEC, EDGES, VPT, WARP, THREADS>;
-  static std::atomic<bool> done[kMaxDevices] = {};
-  static std::atomic<int> known[33] = {};
+  static KernelFacts facts[kMaxDevices] = {};
   const int bytes = RowRing<T, VEC, EDGES, VPT, 3>::place_bytes(p.threads);
   const int places = ring_places(bytes, PLACES_BACKWARD);
   const int w_bytes = VPT * VEC * 4 * (WARP ? 32 : p.threads);
   const int w_smem = places * bytes + w_bytes <= NORM_BLOCK_SMEM;
   const int smem = places * bytes + (w_smem ? w_bytes : 0);
   int per_sm = 0;
-  cudaError_t e = allow_smem(kern, done);
-  if (e == cudaSuccess) e = resident(kern, known, p.threads, smem, &per_sm);
+  cudaError_t e = resident(kern, facts, p.threads, smem, &per_sm);
   if (e != cudaSuccess) return e;
   const int most = std::min(backward_most(p, a.T, num_sms), per_sm * num_sms);
   const int grid = row_blocks(p, a.T, a.classes, most);
