@@ -504,7 +504,8 @@ kd_status kd_embedding_forward(const kd_embedding_problem* prob, const void* W, 
  *                            when accumulate_dW != 0 (those rows are not touched): with
  *                            a tied head, the dW that its backward wrote
  * The rows of one id are added in fp32 in the order of their tokens, in runs of
- * 32, and the runs in their order: the same bits every time. */
+ * 32, and the runs in their order: the same bits every time. (What is added to, and the sums
+ * added, are taken as zero below 2^-126: the device adds so in memory.) */
 kd_status kd_embedding_backward(const kd_embedding_problem* prob, const void* dY,
                                 const int32_t* ids, const uint8_t* mask, float* dW,
                                 int accumulate_dW, void* workspace, size_t workspace_bytes,
@@ -517,7 +518,9 @@ kd_status kd_embedding_backward(const kd_embedding_problem* prob, const void* dY
  *   y = n weight + bias                   (bias: KD_NORM_LAYER only)
  * Backward, with g = dy weight:
  *   dx = rstd (g - n mean(g n) [- mean(g): layer]) + dh    (for x and residual alike)
- *   dweight = sum over rows of dy n,  dbias = sum over rows of dy (KD_NORM_LAYER only) */
+ *   dweight = sum over rows of dy n,  dbias = sum over rows of dy (KD_NORM_LAYER only)
+ * Sums over a row, of squares too, are formed in fp32 and have its range: magnitudes of some 1e17
+ * and more overflow them, and rows below some 1e-19, whose squares vanish, need an eps above 0. */
 enum { KD_NORM_LAYER = 0, KD_NORM_RMS = 1 };
 
 typedef struct {
@@ -590,13 +593,17 @@ typedef struct {
   int32_t param_bf16, grad_bf16;
 } kd_muon_options;
 
-/* Workspace bytes of a step over these matrices (only their sizes are read): up to 16
- * bytes for each element of as many matrices as are worked on at a time. 0 if a size is invalid. */
+/* Workspace bytes of a step over these matrices (only their sizes are read); 0 if one is invalid.
+ * Matrices that are worked on together (below) have their workspace at the same time: with r <= k
+ * the sizes of one and r', k' these rounded up to multiples of 64, 8 r (r' + k') bytes, 12 for
+ * every 16,384 elements, and up to 1 KB for each shape. Small matrices alone take 256 bytes. */
 size_t kd_muon_workspace_size(const kd_muon_matrix* matrices, int32_t n_matrices);
 
-/* `matrices` is a host array; it is read before the call returns. Up to 384 matrices of up to 16
- * shapes that follow one another go through the step's 17 launches together: sort them by
- * shape. A wait that ran out is reported as KD_ERR_TIMEOUT by kd_kl_check_status. */
+/* `matrices` is a host array; it is read before the call returns. Matrices are worked on in
+ * rounds of 2 + 3 steps launches: up to 384 that follow one another, of up to 16 shapes, with at
+ * most 3 GiB of workspace (or one matrix that needs more): sort them by shape. Where all are at
+ * most 128 x 256 or 256 x 128, a launch takes 384 of them through all steps. A wait that ran out is
+ * reported as KD_ERR_TIMEOUT by kd_kl_check_status. */
 kd_status kd_muon_step(const kd_muon_matrix* matrices, int32_t n_matrices,
                        const kd_muon_options* opts, void* workspace, size_t workspace_bytes,
                        void* stream);
