@@ -845,7 +845,7 @@ __global__ void __launch_bounds__(PRODUCT_THREADS, 1)
 // the whole step in one launch, X and S as halves in shared memory, each product one
 // accumulator. X's blocks of 64 columns are the first factors' layout (K-major) of S = X X^T and,
 // read the other way, the second factor's (MN-major) of P X. 14 matrices of 96 x 96 and
-// 96 x 250 take 63 us so and 230 by the launches above, each of which waits for its
+// 96 x 250 take 61 us so and 226 by the launches above, each of which waits for its
 // tiles' loads, products and stores one after the other.
 
 constexpr int SMALL_THREADS = 512;

@@ -45,7 +45,7 @@ constexpr int KIND_LAYER = 0;       // KD_NORM_LAYER
 // backward are 35 to 70 KB in flight on an SM.
 constexpr int PLACES_FORWARD = 3, PLACES_BACKWARD = 2;
 // Forward: rows of a block, at most, where a row is a block's. Blocks that come and go even
-// out what SMs differ by: 32,768 rows of 2880 bf16 take 116 us so, and 120 to 150 (by their
+// out what SMs differ by: 32,768 rows of 2880 bf16 take 113 us so, and 120 to 150 (by their
 // number) with blocks that stay.
 constexpr int ROWS_FORWARD = 8;
 // Backward: each block leaves a row of sums, so blocks stay. Threads on an SM: 123 us at 1160,
